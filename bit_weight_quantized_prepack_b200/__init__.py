@@ -23,6 +23,8 @@ __all__ = [
     "wq_prepack_act_order", "wq_permute_act", "wq_gemm_w4a16_act_order",
     "wq_prepacked_bytes_sparse24", "wq_prepack_sparse24", "wq_unpack_sparse24", "wq_gemm_w4a16_sparse24",
     "wq_prepacked_bytes_mixed", "wq_prepack_mixed", "wq_unpack_mixed", "wq_gemm_w4a16_mixed",
+    "wq_route_experts", "wq_expert_lists", "wq_prepacked_bytes_experts", "wq_prepack_experts", "wq_unpack_experts",
+    "wq_gemm_w4a16_experts", "wq_experts_scratch_bytes", "wq_gemm_w4a16_experts_combine",
     "wq_workspace_bytes", "wq_workspace_reserve", "wq_get_device_status", "wq_plan", "wq_plan_for",
     "wq_debug_set_wait_timeout_ns", "wq_debug_skip_publish",
     "WQ_OK", "WQ_ERR_INVALID_ARG", "WQ_ERR_UNSUPPORTED_SHAPE", "WQ_ERR_MISALIGNED",
@@ -83,6 +85,14 @@ def _load():
         "wq_prepack_mixed": (I, [P, P, P, I, I, I, P, Z, P]),
         "wq_unpack_mixed": (I, [P, I, I, I, P, P, P, P]),
         "wq_gemm_w4a16_mixed": (I, [P, P, Z, P, I, I, I, I, P]),
+        "wq_route_experts": (I, [P, I, P, I, I, I, I, I, I, I, I, ctypes.c_float, P, P, P, P, P]),
+        "wq_expert_lists": (I, [P, I, I, I, P, P, P]),
+        "wq_prepacked_bytes_experts": (Z, [I, I, I, I]),
+        "wq_prepack_experts": (I, [P, P, I, I, I, I, I, P, P]),
+        "wq_unpack_experts": (I, [P, I, I, I, I, I, P, P, P]),
+        "wq_gemm_w4a16_experts": (I, [P, P, P, P, P, I, I, I, I, I, I, I, P]),
+        "wq_experts_scratch_bytes": (Z, [I, I, I]),
+        "wq_gemm_w4a16_experts_combine": (I, [P, P, P, P, P, P, P, P, Z, I, I, I, I, I, I, P]),
         "wq_workspace_bytes": (Z, [I, I, I, I]),
         "wq_workspace_reserve": (I, [Z, P]),
         "wq_get_device_status": (I, [P]),
@@ -587,6 +597,202 @@ def wq_gemm_w4a8_fp16act(A: torch.Tensor, Wp: torch.Tensor, sw: torch.Tensor, N:
         Y = torch.empty((M, N), dtype=torch.float16, device=A.device)
     _check(lib.wq_gemm_w4a8_fp16act(_ptr(A), _ptr(Wp), _ptr(sw), _ptr(Y), _ptr(acc_out), _ptr(sa_out), M, N, K,
                                     act_bits, _stream(stream)), "wq_gemm_w4a8_fp16act")
+    return Y
+
+
+# ------------------------------------------------------------------ experts
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _device_call(dev, stream, name, *args):
+    """One library call on the tensors' device and, without a stream, on that device's current one."""
+    f = getattr(lib, name)
+    if dev.index == torch.cuda.current_device():
+        _check(f(*args, _stream(stream)), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(f(*args, _stream(stream)), name)
+
+
+def _scratch(nbytes, dev, stream):
+    """Scratch of one call, allocated on the stream that the call runs on: it is handed out again
+    only to later work of that stream, and inside a graph capture it belongs to the graph."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+
+
+def wq_route_experts(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None = None, score: str = "softmax",
+                     groups: int = 1, top_groups: int = 1, group_top: int = 1, renorm: bool = True,
+                     scale: float = 1.0, lists: bool = False, idx: torch.Tensor | None = None,
+                     w: torch.Tensor | None = None, stream=None):
+    """Choose top_k experts per token: logits fp16 or fp32 [T, E] -> idx int32 [T, top_k], w fp32
+    [T, top_k], and with ``lists`` also (offsets, rows) as wq_expert_lists gives them.
+
+    ``score`` "softmax" or "sigmoid"; ``bias`` fp32 [E] is added to the scores for the choice only;
+    of ``groups`` runs of experts the ``top_groups`` with the largest sum of their ``group_top``
+    best stay; the weights are divided by their sum (``renorm``) and multiplied by ``scale``."""
+    T, E = _matrix(logits, "logits")
+    if logits.dtype not in (torch.float16, torch.float32):
+        raise TypeError(f"logits must be torch.float16 or torch.float32, got {logits.dtype}")
+    _tensor(logits, logits.dtype, "logits")
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
+    if top_k <= 0:
+        raise WqError(WQ_ERR_INVALID_ARG, "wq_route_experts")
+    if bias is not None:
+        _tensor(bias, torch.float32, "bias", shape=(E,))
+    if idx is not None:
+        _tensor(idx, torch.int32, "idx", shape=(T, top_k))
+    if w is not None:
+        _tensor(w, torch.float32, "w", shape=(T, top_k))
+    _on_one_cuda_device(logits=logits, bias=bias, idx=idx, w=w)
+    dev = logits.device
+    if idx is None:
+        idx = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    if w is None:
+        w = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    offsets = torch.empty((E + 1,), dtype=torch.int32, device=dev) if lists else None
+    rows = torch.empty((T * top_k,), dtype=torch.int32, device=dev) if lists else None
+    _device_call(dev, stream, "wq_route_experts", _ptr(logits), int(logits.dtype == torch.float32), _ptr(bias), T, E,
+                 top_k, _SCORES[score], groups, top_groups, group_top, int(bool(renorm)), scale, _ptr(idx), _ptr(w),
+                 _ptr(offsets), _ptr(rows))
+    return (idx, w, offsets, rows) if lists else (idx, w)
+
+
+def wq_expert_lists(idx: torch.Tensor, E: int, offsets: torch.Tensor | None = None, rows: torch.Tensor | None = None,
+                    stream=None):
+    """The pairs t * top_k + j by expert: idx int32 [T, top_k] -> offsets int32 [E + 1], rows int32
+    [T * top_k]; pairs whose idx lies outside [0, E) are in no list."""
+    T, top_k = _matrix(idx, "idx")
+    _tensor(idx, torch.int32, "idx")
+    if offsets is not None:
+        _tensor(offsets, torch.int32, "offsets", shape=(E + 1,))
+    if rows is not None:
+        _tensor(rows, torch.int32, "rows", shape=(T * top_k,))
+    _on_one_cuda_device(idx=idx, offsets=offsets, rows=rows)
+    if offsets is None:
+        offsets = torch.empty((max(E, 0) + 1,), dtype=torch.int32, device=idx.device)
+    if rows is None:
+        rows = torch.empty((T * top_k,), dtype=torch.int32, device=idx.device)
+    _device_call(idx.device, stream, "wq_expert_lists", _ptr(idx), T, E, top_k, _ptr(offsets), _ptr(rows))
+    return offsets, rows
+
+
+def wq_prepacked_bytes_experts(E: int, K: int, N: int, g: int) -> int:
+    return lib.wq_prepacked_bytes_experts(E, K, N, g)
+
+
+def _experts_size(E, K, N, g, gated, where):
+    n = wq_prepacked_bytes_experts(E, K, N, g)
+    if E <= 0 or K <= 0 or N <= 0:
+        raise WqError(WQ_ERR_INVALID_ARG, where)
+    if gated and N % 16:
+        raise WqError(WQ_ERR_UNSUPPORTED_SHAPE, where)
+    if n == 0:  # the counts and shapes are those of any prepacked weight, else it is the group size
+        raise WqError(WQ_ERR_UNSUPPORTED_SHAPE if E > 1024 or K % 128 or N % 8 else WQ_ERR_INVALID_ARG, where)
+    return n
+
+
+def wq_prepack_experts(Q: torch.Tensor, s: torch.Tensor, g: int, gated: bool = False, Wp: torch.Tensor | None = None,
+                       stream=None):
+    """Q int32 [E, K/8, N], s fp16 [E, K/g, N] -> Wp uint8 [wq_prepacked_bytes_experts(E, K, N, g)].
+    ``gated``: the columns are [gate | up]."""
+    if not isinstance(Q, torch.Tensor) or Q.dim() != 3:
+        raise ValueError("Q must be a 3-D tensor")
+    E, K8, N = Q.shape
+    K = K8 * 8
+    _tensor(Q, torch.int32, "Q")
+    nbytes = _experts_size(E, K, N, g, gated, "wq_prepack_experts")
+    _tensor(s, torch.float16, "s", shape=(E, K // g, N))
+    if Wp is not None:
+        _tensor(Wp, torch.uint8, "Wp", min_numel=nbytes)
+    _on_one_cuda_device(Q=Q, s=s, Wp=Wp)
+    if Wp is None:
+        Wp = torch.empty(nbytes, dtype=torch.uint8, device=Q.device)
+    _device_call(Q.device, stream, "wq_prepack_experts", _ptr(Q), _ptr(s), E, K, N, g, int(bool(gated)), _ptr(Wp))
+    return Wp
+
+
+def wq_unpack_experts(Wp: torch.Tensor, E: int, K: int, N: int, g: int, gated: bool = False, stream=None):
+    """Inverse of wq_prepack_experts: (Q int32 [E, K/8, N], s fp16 [E, K/g, N])."""
+    _tensor(Wp, torch.uint8, "Wp", min_numel=_experts_size(E, K, N, g, gated, "wq_unpack_experts"))
+    _on_one_cuda_device(Wp=Wp)
+    Q = torch.empty((E, K // 8, N), dtype=torch.int32, device=Wp.device)
+    s = torch.empty((E, K // g, N), dtype=torch.float16, device=Wp.device)
+    _device_call(Wp.device, stream, "wq_unpack_experts", _ptr(Wp), E, K, N, g, int(bool(gated)), _ptr(Q), _ptr(s))
+    return Q, s
+
+
+def _experts_args(A, Wp, offsets, rows, N, g, gated, where):
+    A_rows, K = _matrix(A, "A" if where == "wq_gemm_w4a16_experts" else "H")
+    _tensor(A, torch.float16, "A" if where == "wq_gemm_w4a16_experts" else "H")
+    _tensor(offsets, torch.int32, "offsets")
+    _tensor(rows, torch.int32, "rows")
+    if offsets.dim() != 1 or rows.dim() != 1:
+        raise ValueError("offsets and rows must be 1-D")
+    E = offsets.numel() - 1
+    _tensor(Wp, torch.uint8, "Wp", min_numel=_experts_size(E, K, N, g, gated, where))
+    return A_rows, K, E
+
+
+def wq_gemm_w4a16_experts(A: torch.Tensor, Wp: torch.Tensor, offsets: torch.Tensor, rows: torch.Tensor, N: int, g: int,
+                          gated: bool = False, Y: torch.Tensor | None = None, stream=None):
+    """Every pair's token row times its expert's weight: A fp16 [T, K] -> Y fp16 [T * top_k, N], or
+    [T * top_k, N / 2] = silu(gate) * up when ``gated`` (N counts both halves). offsets [E + 1] and
+    rows [T * top_k] are the lists by expert; rows of Y of pairs in no list are left as they were."""
+    T, K, E = _experts_args(A, Wp, offsets, rows, N, g, gated, "wq_gemm_w4a16_experts")
+    pairs = rows.numel()
+    if T == 0 or pairs % T:
+        if T or pairs:
+            raise ValueError(f"rows holds {pairs} pairs, not a multiple of A's {T} rows")
+    top_k = pairs // T if T else 1
+    shape = (pairs, N // 2 if gated else N)
+    if Y is not None:
+        _tensor(Y, torch.float16, "Y", shape=shape)
+    _on_one_cuda_device(A=A, Wp=Wp, offsets=offsets, rows=rows, Y=Y)
+    if Y is None:
+        Y = torch.empty(shape, dtype=torch.float16, device=A.device)
+    if pairs:
+        _device_call(A.device, stream, "wq_gemm_w4a16_experts", _ptr(A), _ptr(Wp), _ptr(offsets), _ptr(rows), _ptr(Y),
+                     T, E, top_k, N, K, g, int(bool(gated)))
+    return Y
+
+
+def wq_experts_scratch_bytes(T: int, top_k: int, N: int) -> int:
+    return lib.wq_experts_scratch_bytes(T, top_k, N)
+
+
+def wq_gemm_w4a16_experts_combine(H: torch.Tensor, Wp: torch.Tensor, idx: torch.Tensor, w: torch.Tensor,
+                                  offsets: torch.Tensor, rows: torch.Tensor, N: int, g: int,
+                                  Y: torch.Tensor | None = None, scratch: torch.Tensor | None = None, stream=None):
+    """Y fp16 [T, N] = sum over j of w[t, j] * (H[t * top_k + j] . W[idx[t, j]]); H fp16 [T * top_k, K]
+    by pair, idx and w [T, top_k], the lists those of idx. Choices outside [0, E) add nothing."""
+    T, top_k = _matrix(idx, "idx")
+    pairs, K, E = _experts_args(H, Wp, offsets, rows, N, g, False, "wq_gemm_w4a16_experts_combine")
+    _tensor(idx, torch.int32, "idx")
+    _tensor(w, torch.float32, "w", shape=(T, top_k))
+    if top_k == 0:
+        raise WqError(WQ_ERR_INVALID_ARG, "wq_gemm_w4a16_experts_combine")
+    if pairs != T * top_k:
+        raise ValueError(f"H must have {T * top_k} rows (one per pair), got {pairs}")
+    _tensor(rows, torch.int32, "rows", shape=(pairs,))
+    if Y is not None:
+        _tensor(Y, torch.float16, "Y", shape=(T, N))
+    nbytes = wq_experts_scratch_bytes(T, top_k, N) if pairs else 0
+    if scratch is not None:
+        _tensor(scratch, torch.uint8, "scratch", min_numel=nbytes)
+    _on_one_cuda_device(H=H, Wp=Wp, idx=idx, w=w, offsets=offsets, rows=rows, Y=Y, scratch=scratch)
+    if Y is None:
+        Y = torch.empty((T, N), dtype=torch.float16, device=H.device)
+    if pairs:
+        if scratch is None:
+            scratch = _scratch(nbytes, H.device, stream)
+        _device_call(H.device, stream, "wq_gemm_w4a16_experts_combine", _ptr(H), _ptr(Wp), _ptr(idx), _ptr(w),
+                     _ptr(offsets), _ptr(rows), _ptr(Y), _ptr(scratch), scratch.numel(), T, E, top_k, N, K, g)
     return Y
 
 

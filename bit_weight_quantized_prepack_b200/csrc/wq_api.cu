@@ -12,6 +12,7 @@
 #include <utility>
 
 #include "wq.h"
+#include "wq_experts.h"
 #include "wq_internal.h"
 
 namespace {
@@ -70,6 +71,7 @@ DeviceState* device_state(int* dev_out) {
         if (cudaMemset(d.status, 0, sizeof(int)) != cudaSuccess) return nullptr;
         if (cudaMalloc(&d.check, sizeof(int)) != cudaSuccess) return nullptr;
         if (configure_gemm_kernels(d.smem_optin - 2048) != cudaSuccess) return nullptr;
+        if (configure_expert_kernels() != cudaSuccess) return nullptr;
     }
     if (!g_encode) {
         void* fn = nullptr;
@@ -408,6 +410,23 @@ int noalloc_device(int* dev_out, NoAllocDevice** out) {
 }
 
 }  // namespace
+
+namespace wq {
+
+int acquire_device(cudaStream_t stream, DeviceInfo* info) {
+    std::lock_guard<std::mutex> lock(g_mu);
+    int dev = 0;
+    DeviceState* d = nullptr;
+    const int rc = require_device(&dev, &d, stream, true);
+    if (rc) return rc;
+    info->num_sms = d->num_sms;
+    info->status = d->status;
+    info->encode = reinterpret_cast<void*>(g_encode);
+    info->timeout_ns = g_timeout_ns;
+    return WQ_OK;
+}
+
+}  // namespace wq
 
 extern "C" {
 

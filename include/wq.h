@@ -274,6 +274,76 @@ WQ_API int wq_gemm_w4a8_fp16act(const uint16_t* A, const void* Wp, const float* 
 WQ_API int wq_gemm_w4a16_noalloc(const uint16_t* A, const void* Wp, uint16_t* Y,
                   int M, int N, int K, int g, void* stream);
 
+/* ---------------------------------------------------------------- experts
+ * A sparse-expert layer with 4-bit weights: each of T tokens takes top_k of E experts, and each
+ * expert is a W4A16 weight of its own. A PAIR is p = t * top_k + j, token t's j-th choice. A
+ * layer is: wq_route_experts (choices, weights, lists), wq_gemm_w4a16_experts (the up product,
+ * gated), wq_gemm_w4a16_experts_combine (the down product, summed over a token's choices).
+ * ("Atom: Low-bit Quantization for Efficient and Accurate LLM Serving", method: fine-grained
+ * group quantisation, here of every expert's weight; the routing is not in the pages.)
+ * Limits: 1 <= E <= 1024, 1 <= top_k <= min(E, 32), 0 <= T <= 2^24, T * top_k <= 2^28; T == 0
+ * computes nothing. Alignment: A, H, Wp, Y, Q, s, scratch 16 bytes; idx, w, bias, offsets, rows
+ * and fp32 logits 4 bytes, fp16 logits 2 bytes. No call here uses the library's workspace, so
+ * calls and captured graphs that run at the same time share nothing but what the caller gives
+ * them both. Results are deterministic.
+ *
+ * wq_route_experts: logits [T, E], fp16 (logits_fp32 0) or fp32 (1). The scores p are softmax
+ * (score 0; over the row's finite logits) or sigmoid (score 1) of the logits; bias (fp32 [E],
+ * nullable) is added for the choice only: c = p + bias. The E experts are `groups` runs of
+ * E / groups; when top_groups < groups, the top_groups groups with the largest sum of their
+ * group_top (1 or 2) largest c stay and the others are left out. Of the experts that stay the
+ * top_k with the largest c are chosen, in that order; ties go to the lowest index (groups too).
+ * Without a bias the experts are ordered by the logits themselves. c and the sums are held in 64
+ * bits. w[t, j] is the chosen expert's p (never the bias), divided by their sum when renorm is 1
+ * (0 when that sum is 0), times scale; computed in 64 bits, rounded once to fp32. An expert whose
+ * logit or bias is not finite is never chosen (a bias of -inf turns an expert off); where fewer
+ * than top_k are left, idx is -1 and w 0 in the places behind them. idx int32 [T, top_k], w fp32
+ * [T, top_k]. offsets and rows (both or neither null): as wq_expert_lists on idx.
+ * top_k <= top_groups * (E / groups); groups divides E, groups <= 64.
+ *
+ * wq_expert_lists: the pairs by expert. offsets int32 [E + 1]: the pairs of expert e are
+ * rows[offsets[e]] .. rows[offsets[e + 1] - 1], in ascending order. A pair whose idx lies outside
+ * [0, E) (a padded place, an expert that another device holds) is in no list; rows int32
+ * [T * top_k] is left as it was from offsets[E] on.
+ *
+ * wq_prepacked_bytes_experts / wq_prepack_experts / wq_unpack_experts: Q int32 [E, K/8, N], s
+ * fp16 [E, K/g, N] -> Wp (all experts, K, N and g as for wq_prepack) and back (test aid). With
+ * gated 1 the N = 2I columns are [gate | up] (I a multiple of 8), stored so that a gate column
+ * meets its up column in one thread. Unlike wq_prepack's, the buffer suits the expert products
+ * only, and each product wants the gated flag that its buffer was laid out with.
+ *
+ * wq_gemm_w4a16_experts: for every pair p in the lists, with e its expert,
+ *   gated 0: Y[p, n] = A[p / top_k] . W_e[:, n]                        Y fp16 [T * top_k, N]
+ *   gated 1: Y[p, i] = silu(gate) * up, gate = A[p / top_k] . W_e[:, i],
+ *            up = A[p / top_k] . W_e[:, I + i]                         Y fp16 [T * top_k, I]
+ * A fp16 [T, K]; products of exact (q - 8) or of weights rounded once to fp16, fp32 sums, Y
+ * rounded once. Rows of Y of pairs that are in no list are left as they were. The lists are read
+ * on the device: an entry of rows outside [0, T * top_k) is skipped and records
+ * WQ_ERR_INVALID_ARG in the device status word (wq_get_device_status), offsets are taken as if
+ * clamped to [0, T * top_k] and made non-decreasing; a pair listed twice leaves its row of Y
+ * unspecified. Y must not overlap A.
+ *
+ * wq_gemm_w4a16_experts_combine: Y[t, n] = sum over j of w[t, j] * (H[t * top_k + j] . W_e[:, n]),
+ * e = idx[t, j]; choices outside [0, E) add nothing (a token without any gets zeros). H fp16
+ * [T * top_k, K] by pair, Y fp16 [T, N], and idx, w and the lists as wq_route_experts gives them
+ * (the lists are those of idx). The sum runs over j in order, in fp32. scratch:
+ * wq_experts_scratch_bytes(T, top_k, N) bytes that the call may write until it has completed. */
+WQ_API int wq_route_experts(const void* logits, int logits_fp32, const float* bias, int T, int E, int top_k, int score,
+                 int groups, int top_groups, int group_top, int renorm, float scale, int32_t* idx, float* w,
+                 int32_t* offsets, int32_t* rows, void* stream);
+WQ_API int wq_expert_lists(const int32_t* idx, int T, int E, int top_k, int32_t* offsets, int32_t* rows, void* stream);
+WQ_API size_t wq_prepacked_bytes_experts(int E, int K, int N, int g);
+WQ_API int wq_prepack_experts(const int32_t* Q, const uint16_t* s, int E, int K, int N, int g, int gated, void* Wp,
+                 void* stream);
+WQ_API int wq_unpack_experts(const void* Wp, int E, int K, int N, int g, int gated, int32_t* Q_out, uint16_t* s_out,
+                 void* stream);
+WQ_API int wq_gemm_w4a16_experts(const uint16_t* A, const void* Wp, const int32_t* offsets, const int32_t* rows,
+                 uint16_t* Y, int T, int E, int top_k, int N, int K, int g, int gated, void* stream);
+WQ_API size_t wq_experts_scratch_bytes(int T, int top_k, int N);
+WQ_API int wq_gemm_w4a16_experts_combine(const uint16_t* H, const void* Wp, const int32_t* idx, const float* w,
+                 const int32_t* offsets, const int32_t* rows, uint16_t* Y, void* scratch, size_t scratch_bytes,
+                 int T, int E, int top_k, int N, int K, int g, void* stream);
+
 /* ---------------------------------------------------------------- workspace and status
  * Bytes of library workspace one call of the given kind and shape needs (kind 0 = W4A16,
  * 1 = W4A8, 2 = W4A8 on fp16 activations, wq_gemm_w4a8_fp16act, 3 = wq_gemm_w4a16_zp,

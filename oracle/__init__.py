@@ -5,4 +5,5 @@ benchmark import it; the library never does. See ``wq_oracle`` for what it
 computes and which page each step follows.
 """
 from .wq_oracle import *  # noqa: F401,F403
-from . import wq_oracle  # noqa: F401
+from .wq_experts_oracle import *  # noqa: F401,F403
+from . import wq_experts_oracle, wq_oracle  # noqa: F401
