@@ -87,7 +87,9 @@ cudaError_t launch_prepack_experts(const int32_t* Q, const uint16_t* s, int E, i
 cudaError_t launch_unpack_experts(const void* Wp, int E, int K, int N, int g, int gated, int32_t* Q, uint16_t* s,
                                   cudaStream_t st);
 cudaError_t configure_expert_kernels();
-cudaError_t launch_experts(const ExpertArgs& a, int num_sms, cudaStream_t st);
+cudaError_t configure_experts_large();
+cudaError_t launch_experts(const ExpertArgs& a, const DeviceInfo& d, cudaStream_t st);
+cudaError_t launch_experts_large(const ExpertArgs& a, const DeviceInfo& d, cudaStream_t st);
 cudaError_t launch_combine_experts(const uint16_t* yp, const int32_t* idx, const float* w, int T, int top_k, int E,
                                    int N, uint16_t* Y, cudaStream_t st);
 

@@ -60,7 +60,7 @@ int run_products(const uint16_t* A, const void* Wp, const int32_t* offsets, cons
     a.K = K;
     a.g = g;
     a.gated = gated;
-    return status_of(launch_experts(a, d->num_sms, st));
+    return status_of(launch_experts(a, *d, st));
 }
 
 }  // namespace

@@ -1,0 +1,81 @@
+// Device code that the expert products share: dequantisation, the table of tiles, the gate.
+#pragma once
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "wq_experts.h"
+#include "wq_ptx.cuh"
+
+namespace wq {
+
+constexpr unsigned kFull = 0xFFFFFFFFu;
+
+// The four fp16 pairs (rows 0..7) of one code word as exact q - 8: a nibble under the exponent of
+// 1024 is 1024 + q (low) or 1024 + 16q (high).
+__device__ __forceinline__ void dequant8(uint32_t w, uint32_t (&p)[4]) {
+    const __half2 low = __halves2half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408));    // 1032
+    const __half2 mul = __halves2half2(__ushort_as_half(0x2C00), __ushort_as_half(0x2C00));    // 1/16
+    const __half2 off = __halves2half2(__ushort_as_half(0xD480), __ushort_as_half(0xD480));    // -72
+    const uint32_t w8 = w >> 8;
+    uint32_t t[4] = {lop3_and_or(w, 0x000F000Fu, 0x64006400u), lop3_and_or(w, 0x00F000F0u, 0x64006400u),
+                     lop3_and_or(w8, 0x000F000Fu, 0x64006400u), lop3_and_or(w8, 0x00F000F0u, 0x64006400u)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        __half2 h = *reinterpret_cast<__half2*>(&t[i]);
+        h = (i & 1) ? __hfma2(h, mul, off) : __hsub2(h, low);
+        p[i] = *reinterpret_cast<uint32_t*>(&h);
+    }
+}
+
+// Rows of each expert from the offsets, clamped into [0, pairs] and made non-decreasing, so that
+// no content of the lists leads outside them: s_start[e] first place, s_tiles[e] tiles before e.
+template <int kBlock>
+__device__ void expert_table(const int32_t* offsets, int E, int pairs, int tile_rows, int* s_start, int* s_tiles,
+                             int* s_scratch) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int kW = kBlock / 32;
+    int carry = 0;  // largest offset so far
+    for (int base = 0; base <= E; base += kBlock) {
+        const int e = base + tid;
+        int v = e <= E ? min(max(__ldg(offsets + e), 0), pairs) : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(kFull, v, o);
+            if (lane >= o) v = max(v, u);
+        }
+        if (lane == 31) s_scratch[warp] = v;
+        __syncthreads();
+        for (int i = 0; i < warp; ++i) v = max(v, s_scratch[i]);
+        v = max(v, carry);
+        if (e <= E) s_start[e] = v;
+        for (int i = 0; i < kW; ++i) carry = max(carry, s_scratch[i]);
+        __syncthreads();
+    }
+    int sum = 0;  // tiles before this block's first expert
+    for (int base = 0; base < E; base += kBlock) {
+        const int e = base + tid;
+        const int own = e < E ? (s_start[e + 1] - s_start[e] + tile_rows - 1) / tile_rows : 0;
+        int v = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(kFull, v, o);
+            if (lane >= o) v += u;
+        }
+        if (lane == 31) s_scratch[warp] = v;
+        __syncthreads();
+        int before = sum;
+        for (int i = 0; i < kW; ++i) {
+            if (i < warp) before += s_scratch[i];
+            sum += s_scratch[i];
+        }
+        if (e < E) s_tiles[e] = before + v - own;
+        __syncthreads();
+    }
+    if (tid == 0) s_tiles[E] = sum;
+    __syncthreads();
+}
+
+__device__ __forceinline__ float silu_mul(float gate, float up) { return gate / (1.0f + __expf(-gate)) * up; }
+
+}  // namespace wq
