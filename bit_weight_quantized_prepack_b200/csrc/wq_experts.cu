@@ -5,9 +5,9 @@
 // experts_kernel (few rows per expert). Tile: 32 columns of one expert x up to 8*NB of its rows,
 // all of K. Eight warps take the tile's 128-row k-blocks in turn; a warp needs nothing from the
 // others until the sums are added, in the order of the warps, at the end. Every lane copies with
-// cp.async exactly the bytes that it will itself multiply (four 16-byte chunks of codes, its
-// scales, 4*NB chunks of activations per k-block) into its own places of a ring in shared memory,
-// so that the ring needs no barrier. The weight is the 16-row operand of m16n8k16 (exact fp16
+// cp.async the codes and scales that it will itself multiply and its share of the activations (four
+// 16-byte chunks of codes, 4*NB of activations per k-block) into its warp's ring in shared memory,
+// so that the ring needs no barrier beyond the warp's. The weight is the 16-row operand of m16n8k16 (exact fp16
 // q - 8), the tokens are its 8 columns; each group's fp32 partial is scaled in fp32, so no weight
 // is rounded.
 #include <cuda_runtime.h>
@@ -35,6 +35,17 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Four 8 x 8 fp16 matrices: lane l gives the address of row l % 8 of matrix l / 8 and receives
+// elements (l / 4, 2 (l % 4)) and the next of each.
+__device__ __forceinline__ uint4 ldmatrix4(const void* row) {
+    uint4 v;
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(smem_addr(row))
+                 : "memory");
+    return v;
 }
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -103,7 +114,7 @@ __global__ void __launch_bounds__(kThreads) experts_kernel(ExpertArgs a, int sta
                     if (arow[b]) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
-                            cp_async16(st + (4 + b * 4 + c) * 512 + lane * 16, arow[b] + kb * kTileK + c * 32);
+                            cp_async16(st + (4 + b * 4 + c) * 512 + q * 128 + gc * 16, arow[b] + kb * kTileK + c * 32);
                     }
                 if (SL) {
 #pragma unroll
@@ -130,6 +141,7 @@ __global__ void __launch_bounds__(kThreads) experts_kernel(ExpertArgs a, int sta
             kb_issue += kWarps;
             // all groups but the newest stages - 1 have arrived
             if (stages == 2) cp_async_wait<1>(); else if (stages == 3) cp_async_wait<2>(); else cp_async_wait<3>();
+            __syncwarp();
             const uint8_t* st = ring + slot * kStage;
             uint4 w[4];
 #pragma unroll
@@ -148,8 +160,8 @@ __global__ void __launch_bounds__(kThreads) experts_kernel(ExpertArgs a, int sta
                 uint4 x[NB];
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
-                    x[b] = make_uint4(0, 0, 0, 0);
-                    if (arow[b]) x[b] = *reinterpret_cast<const uint4*>(st + (4 + b * 4 + c) * 512 + lane * 16);
+                    // rows behind the tile's last are not copied: what lies there meets no stored sum
+                    x[b] = ldmatrix4(st + (4 + b * 4 + c) * 512 + lane * 16);
                 }
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {

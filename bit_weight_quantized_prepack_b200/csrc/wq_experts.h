@@ -4,17 +4,18 @@
 // Prepacked expert weights: E buffers of `expert_stride` bytes, one per expert, each
 //   codes:  unit (u, kb), u < NU = ceil(N/32), kb < K/128, at byte (u*(K/128) + kb) * 2048:
 //     word ((rt*2 + h)*32 + 4*gc + q)*4 + c  (rt, h < 2, gc < 8, q, c < 4) holds the 8 codes of
-//     column v = 32u + 16rt + 8h + gc, rows 128kb + 32c + 8q + j (j = 0..7), code j at nibble
-//     (0, 4, 1, 5, 2, 6, 3, 7)[j]: the order in which one mask gives an fp16 pair of two
+//     column v = 32u + 16rt + 8h + gc, rows 128kb + 32c + 8i + 2q + b (i < 4, b < 2), code
+//     2i + b at nibble (0, 4, 1, 5, 2, 6, 3, 7)[2i + b]: one mask gives the fp16 pair of two
 //     consecutive rows;
 //   scales: after the codes, [NU][K/g groups (1 for g == K)][32] fp16; column v of the unit at
 //     position 4*gc + 2*rt + h.
 //   The buffer is padded to 128 bytes. Columns past N hold code 8 and scale 0 (zero weights).
 // Why this order: lane 4*gc + q of a warp takes the four words c = 0..3 of one (rt, h) with one
-// 16-byte load, a warp's load is 512 contiguous bytes, and the word pair (h = 0, 1) of each c is
-// the weight operand of two m16n8k16 MMAs whose activation operand is 8 consecutive elements of a
-// token's row (32c + 8q ..), so that a quad reads 64 contiguous bytes of it. A lane's scales of
-// its four columns are 8 contiguous bytes.
+// 16-byte load, a warp's load is 512 contiguous bytes, and the pairs i of the words (h = 0, 1) are
+// what that lane holds of the weight both as the 16-row operand of the warp's m16n8k16 (rows 2q,
+// 2q + 1, 2q + 8, 2q + 9 of each 16) and of a 16-lane x 128-bit store to tensor memory (32-bit
+// columns q, 4 + q, ...): K keeps its order, and the activations need no permutation. A lane's
+// scales of its four columns are 8 contiguous bytes.
 // Gated weights ([gate | up], N = 2I): column v is gate column 8(v/16) + v%8 when h = 0, up column
 // the same when h = 1: a lane's two accumulator rows (gc and gc + 8) are the pair that
 // silu(gate) * up needs.

@@ -1,21 +1,26 @@
 // The experts' 4-bit products for many rows per expert: tcgen05 tiles over the lists.
 //
-// Tile: 128 columns of one expert's weight (the MMA's M) x up to 256 of its rows (the MMA's N),
+// Tile: 128 columns of one expert's weight (the MMA's M) x up to 192 of its rows (the MMA's N),
 // all of K in chunks of 64 rows. One persistent CTA per SM, warp-specialised:
-//   warp 0       gathers the rows' 128-byte pieces with TMA gather4 (the lists give the rows);
-//   warp 1       issues the MMAs: both operands from shared memory (128-byte swizzle), fp32
-//                accumulators in tensor memory, two of 256 columns used in turn;
+//   warps 0..3   gather the rows' 128-byte pieces with cp.async into a ring of 8 chunks, four
+//                chunks ahead of what they have signalled;
 //   warps 4..7   epilogue of the tile before, while the next one is multiplied;
-//   warps 8..15  dequantise: each owns 16 columns, loads its codes straight from global memory
-//                several k-blocks ahead (across tiles) and writes fp16 weights (q - 8) * s,
-//                rounded once, into the weight operand's place.
+//   warps 8..15  dequantise: warp 8 + w takes the tile's columns 32 (w % 4) .. + 31 of every second
+//                k-block, loads its codes straight from global memory several k-blocks ahead
+//                (across tiles) and stores fp16 weights (q - 8) * s, rounded once, into one of
+//                four 64-row slots in tensor memory;
+//   warp 16      one elected thread issues the MMAs: weights from tensor memory, rows from shared
+//                memory (128-byte swizzle), fp32 sums in tensor memory, two accumulators of 192
+//                columns used in turn.
 // An expert's rows are split evenly over its row tiles. Tiles of the same rows are neighbours, so
 // that the rows are gathered from L2 after the first time.
-#include <cuda.h>
+// Why so: the weight operand in tensor memory saves the ~32 cycles that each MMA spends on loading
+// it from shared memory (probe, 128 x 256 x 16: 137 cycles against 168), and 192 rows leave tensor
+// memory for a second accumulator. TMA gather4 in place of cp.async moves a row of 128 bytes per 14
+// cycles and set the pace at a quarter of this kernel's rate.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
-#include <cstring>
 
 #include "wq_experts.h"
 #include "wq_experts_dev.cuh"
@@ -25,20 +30,21 @@ namespace wq {
 
 namespace {
 
-constexpr int kLThreads = 512;
-constexpr int kRowsMax = 256;                      // rows of a tile
+constexpr int kLThreads = 17 * 32;
+constexpr int kRowsMax = 192;                      // rows of a tile
 constexpr int kColsL = 128;                        // columns of a tile
 constexpr int kChunkK = 64;                        // weight rows of a stage: one 128-byte swizzle span
-constexpr int kABytes = kColsL * kChunkK * 2;      // 16 KiB
-constexpr int kBBytes = kRowsMax * kChunkK * 2;    // 32 KiB
-constexpr int kStageL = kABytes + kBBytes;
-constexpr int kStagesL = 4;
-constexpr int kSmemL = kStagesL * kStageL + 1024;  // + alignment of the first stage
-constexpr int kDqWarp0 = 8, kDqWarpsL = 8;
-constexpr int kDepth = 4;                          // k-blocks of codes in flight per dequant warp
+constexpr int kBBytes = kRowsMax * kChunkK * 2;    // 24 KiB
+constexpr int kStagesB = 8;
+constexpr int kSlotsA = 4;
+constexpr int kLag = 4;                            // chunks issued after the one that is signalled
+constexpr int kTmemA = 2 * kRowsMax;               // tensor-memory column of the weight slots
+constexpr int kSmemL = kStagesB * kBBytes + 1024;  // + alignment of the first stage
+constexpr int kGatherWarps = 4, kEpiWarp0 = 4, kDqWarp0 = 8, kMmaWarp = 16;
+constexpr int kDepth = 3;                          // k-blocks of codes in flight per dequant warp
 
 struct Bars {
-    uint64_t full_a[kStagesL], full_b[kStagesL], empty[kStagesL];
+    uint64_t full_a[kSlotsA], full_b[kStagesB], empty[kStagesB];
     uint64_t acc_full[2], acc_empty[2], drain;
 };
 
@@ -68,23 +74,20 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, const
     }
 }
 
-// Four rows (any rows of the matrix) x 64 columns, 128 bytes each, to 512 bytes of shared memory.
-__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, int x, int4 r, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(smem_addr(bar))
-        : "memory");
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
 }
 
-// D[tmem] (+)= A[smem] * B[smem]; fp16 inputs, fp32 accumulator.
-__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate) {
+// 16 lanes x 32 columns of 32 bits: lane 4g + q of the warp writes rows g (even registers) and g + 8
+// (odd ones) of columns q, 4 + q, ... 28 + q.
+__device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_t (&v)[16]) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
 
@@ -109,33 +112,53 @@ __device__ __forceinline__ uint4 ldg_stream16(const void* p) {
     return v;
 }
 
-struct TileL {
-    int e, ct, row0, nrows;
-};
+// Walk of a CTA over the tiles: row tile rt_all of all experts' row tiles, column tile ct; column
+// tiles of one row tile are neighbours. CTA b takes tiles b, b + grid, ...
+struct Walk {
+    int rt_all, ct, e;       // position
+    int row0, nrows;         // rows of the tile: places row0 .. of the lists
+    int CT, E, step_rt, step_ct;
+    const int* start;
+    const int* tiles;
 
-// Tile number -> expert, column tile and rows. s_tiles counts row tiles of kRowsMax.
-__device__ __forceinline__ TileL locate(long long tile, int CT, int E, const int* s_start, const int* s_tiles) {
-    const int rt_all = static_cast<int>(tile / CT);
-    TileL t;
-    t.ct = static_cast<int>(tile % CT);
-    int lo = 0, hi = E;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (s_tiles[mid] <= rt_all) lo = mid; else hi = mid;
+    __device__ __forceinline__ Walk(int CT_, int E_, const int* s_start, const int* s_tiles)
+        : e(0), row0(0), nrows(0), CT(CT_), E(E_), start(s_start), tiles(s_tiles) {
+        const unsigned grid = gridDim.x, b = blockIdx.x;
+        step_rt = grid / CT;
+        step_ct = grid % CT;
+        rt_all = b / CT;
+        ct = b % CT;
+        locate();
     }
-    t.e = lo;
-    const int n = s_start[lo + 1] - s_start[lo];
-    const int tiles = s_tiles[lo + 1] - s_tiles[lo];
-    const int each = ((n + tiles - 1) / tiles + 15) / 16 * 16;  // even shares, at most kRowsMax
-    const int first = (rt_all - s_tiles[lo]) * each;
-    t.row0 = s_start[lo] + first;
-    t.nrows = min(each, n - first);
-    return t;
-}
+    __device__ __forceinline__ bool done() const { return rt_all >= tiles[E]; }
+    __device__ __forceinline__ void next() {
+        rt_all += step_rt;
+        ct += step_ct;
+        if (ct >= CT) {
+            ct -= CT;
+            ++rt_all;
+        }
+        locate();
+    }
+    __device__ __forceinline__ void locate() {
+        if (done()) return;
+        int lo = e, hi = E;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (tiles[mid] <= rt_all) lo = mid; else hi = mid;
+        }
+        e = lo;
+        const int n = start[lo + 1] - start[lo], share = tiles[lo + 1] - tiles[lo];
+        const int each = ((n + share - 1) / share + 15) / 16 * 16;  // even shares, at most kRowsMax
+        const int first = (rt_all - tiles[lo]) * each;
+        row0 = start[lo] + first;
+        nrows = min(each, n - first);
+    }
+};
 
 // SL as in the small kernel: scales per k-block and column; 0: per-column, applied in the epilogue.
 template <int SL>
-__global__ void __launch_bounds__(kLThreads, 1) experts_large_kernel(const __grid_constant__ CUtensorMap map, LargeArgs args) {
+__global__ void __launch_bounds__(kLThreads, 1) experts_large_kernel(LargeArgs args) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ Bars bars;
     __shared__ int s_start[kExMaxExperts + 1], s_tiles[kExMaxExperts + 1], s_scratch[kLThreads / 32];
@@ -146,9 +169,9 @@ __global__ void __launch_bounds__(kLThreads, 1) experts_large_kernel(const __gri
     uint8_t* ring = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
 
     if (tid == 0) {
-        for (int i = 0; i < kStagesL; ++i) {
-            mbar_init(&bars.full_a[i], kDqWarpsL);
-            mbar_init(&bars.full_b[i], 1);
+        for (int i = 0; i < kSlotsA; ++i) mbar_init(&bars.full_a[i], 4);
+        for (int i = 0; i < kStagesB; ++i) {
+            mbar_init(&bars.full_b[i], kGatherWarps);
             mbar_init(&bars.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -159,7 +182,7 @@ __global__ void __launch_bounds__(kLThreads, 1) experts_large_kernel(const __gri
         s_stop = 0;
         fence_barrier_init();
     }
-    if (warp == 1) {
+    if (warp == kMmaWarp) {
         tmem_alloc(&s_tmem, 512);
         tmem_relinquish();
     }
@@ -171,78 +194,79 @@ __global__ void __launch_bounds__(kLThreads, 1) experts_large_kernel(const __gri
     const Ctl ctl{&s_stop, a.status, args.timeout_ns};
     const int KT = a.K / kTileK, chunks = a.K / kChunkK;
     const int CT = (a.N + kColsL - 1) / kColsL, NU = ex_units(a.N);
-    const long long tiles = static_cast<long long>(s_tiles[a.E]) * CT;
+    Walk t(CT, a.E, s_start, s_tiles);
 
-    if (warp == 0) {
+    if (warp < kGatherWarps) {
         // ---------------------------------------------------------------- rows of the activations
-        int s = 0;
-        uint32_t ph = 1;  // empty barriers: the first pass over the ring waits for nothing
-        long long issued = 0;
+        // thread (warp, lane): 16-byte piece lane % 8 of rows 16j + 4 warp + lane / 8
+        const int piece = lane & 7, r0 = warp * 4 + (lane >> 3);
+        const uint32_t dst0 = smem_addr(ring) + r0 * 128 + ((piece ^ (r0 & 7)) << 4);
+        unsigned n = 0;  // chunks issued
         bool ok = true;
-        for (long long tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-            const TileL t = locate(tile, CT, a.E, s_start, s_tiles);
-            const int n_mma = (t.nrows + 15) / 16 * 16;
-            int r[8];
+        for (; ok && !t.done(); t.next()) {
+            const uint16_t* src[kRowsMax / 16];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                // rows behind the tile's last repeat it: their sums are never stored
-                const int at = min((i >> 2) * 128 + lane * 4 + (i & 3), t.nrows - 1);
-                const int p = __ldg(a.rows + t.row0 + at);
-                const bool good = static_cast<unsigned>(p) < static_cast<unsigned>(a.pairs);
-                if (!good) atomicCAS(a.status, 0, 1 /* WQ_ERR_INVALID_ARG */);
-                r[i] = good ? p / a.a_div : 0;
+            for (int j = 0; j < kRowsMax / 16; ++j) {
+                // places behind the tile's last row keep what was there: their sums are never stored
+                src[j] = nullptr;
+                if (j * 16 + r0 < t.nrows) {
+                    const int p = __ldg(a.rows + t.row0 + j * 16 + r0);
+                    if (static_cast<unsigned>(p) < static_cast<unsigned>(a.pairs))
+                        src[j] = a.a + static_cast<size_t>(p / a.a_div) * a.K + piece * 8;
+                    else
+                        atomicCAS(a.status, 0, 1 /* WQ_ERR_INVALID_ARG */);
+                }
             }
-            for (int c = 0; c < chunks; ++c) {
-                ok = __all_sync(kFull, wait_phase(&bars.empty[s], ph, ctl));
+            for (int c = 0; c < chunks; ++c, ++n) {
+                ok = __all_sync(kFull, wait_phase(&bars.empty[n % kStagesB], ((n / kStagesB) & 1) ^ 1, ctl));
                 if (!ok) break;
-                uint8_t* b = ring + s * kStageL + kABytes;
-                if (lane == 0) mbar_arrive_expect_tx(&bars.full_b[s], n_mma * kChunkK * 2);
-                __syncwarp();
-                if (lane * 4 < n_mma)
-                    tma_gather4(b + lane * 512, &map, c * kChunkK, make_int4(r[0], r[1], r[2], r[3]), &bars.full_b[s]);
-                if (128 + lane * 4 < n_mma)
-                    tma_gather4(b + (32 + lane) * 512, &map, c * kChunkK, make_int4(r[4], r[5], r[6], r[7]),
-                                &bars.full_b[s]);
-                ++issued;
-                if (++s == kStagesL) {
-                    s = 0;
-                    ph ^= 1;
+                const uint32_t dst = dst0 + (n % kStagesB) * kBBytes;
+#pragma unroll
+                for (int j = 0; j < kRowsMax / 16; ++j)
+                    if (src[j])
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + j * 2048),
+                                     "l"(src[j] + c * kChunkK)
+                                     : "memory");
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                if (n >= kLag) {
+                    asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.full_b[(n - kLag) % kStagesB]);
                 }
             }
         }
-        if (!ok) {
-            // given up: the copies still in flight must land before the CTA leaves
-            for (long long i = issued > kStagesL ? issued - kStagesL : 0; i < issued; ++i)
-                wait_phase(&bars.full_b[i % kStagesL], static_cast<uint32_t>((i / kStagesL) & 1), ctl, false);
-        }
-    } else if (warp == 1) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0)
+            for (unsigned i = n > kLag ? n - kLag : 0; i < n; ++i) mbar_arrive(&bars.full_b[i % kStagesB]);
+    } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------------- MMAs
-        if (lane == 0) {
-            int s = 0, buf = 0;
-            uint32_t ph = 0, aph = 1;
+        // One elected thread runs the whole loop: inside its branch the operands stay uniform (174
+        // cycles per MMA from a thread picked by its number, 40 from an elected one).
+        if (elect_one()) {
+            unsigned n = 0;
+            int buf = 0;
+            uint32_t aph = 1;
             bool ok = true;
-            for (long long tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-                const TileL t = locate(tile, CT, a.E, s_start, s_tiles);
+            const uint64_t desc0 = smem_desc_sw128(smem_addr(ring));
+            for (; ok && !t.done(); t.next()) {
                 const uint32_t idesc = idesc_f16_f32(kColsL, (t.nrows + 15) / 16 * 16);
+                const uint32_t d = tmem + buf * kRowsMax;
                 ok = wait_phase(&bars.acc_empty[buf], aph, ctl);
                 tc_fence_after();
-                for (int c = 0; c < chunks && ok; ++c) {
-                    ok = wait_phase(&bars.full_a[s], ph, ctl) && wait_phase(&bars.full_b[s], ph, ctl);
+                for (int c = 0; c < chunks && ok; ++c, ++n) {
+                    ok = wait_phase(&bars.full_b[n % kStagesB], (n / kStagesB) & 1, ctl) &&
+                         wait_phase(&bars.full_a[n % kSlotsA], (n / kSlotsA) & 1, ctl);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t base = smem_addr(ring + s * kStageL);
-                    uint64_t da = smem_desc_sw128(base), db = smem_desc_sw128(base + kABytes);
+                    const uint64_t db = smem_desc_advance(desc0, (n % kStagesB) * kBBytes);
+                    const uint32_t wa = tmem + kTmemA + (n % kSlotsA) * (kChunkK / 2);
 #pragma unroll
-                    for (int k = 0; k < kChunkK / 16; ++k) {
-                        mma_f16_ss(tmem + buf * kRowsMax, da, db, idesc, (c | k) ? 1u : 0u);
-                        da = smem_desc_advance(da, 32);
-                        db = smem_desc_advance(db, 32);
-                    }
-                    tc_commit(&bars.empty[s]);
-                    if (++s == kStagesL) {
-                        s = 0;
-                        ph ^= 1;
-                    }
+                    for (int k = 0; k < kChunkK / 16; ++k)
+                        mma_f16_ts(d, wa + k * 8, smem_desc_advance(db, k * 32), idesc, (c | k) ? 1u : 0u);
+                    tc_commit(&bars.empty[n % kStagesB]);
                 }
                 if (ok) tc_commit(&bars.acc_full[buf]);
                 buf ^= 1;
@@ -253,14 +277,123 @@ __global__ void __launch_bounds__(kLThreads, 1) experts_large_kernel(const __gri
             wait_phase(&bars.drain, 0, ctl, false);
         }
         __syncwarp();
-    } else if (warp >= 4 && warp < 8) {
+    } else if (warp >= kDqWarp0) {
+        // ---------------------------------------------------------------- weights
+        const int quarter = warp & 3, par = (warp - kDqWarp0) >> 2;
+        const int gc = lane >> 2;
+        constexpr int kS = SL ? SL : 1;
+        uint4 w[kDepth][4];    // [(rt, h)]
+        uint2 sc[kDepth][kS];  // scales of the columns (rt, h) as fp16
+        uint32_t valid = 0, live = 0;  // bit d: slot d holds a k-block / one inside the weight
+        int f_kb = par;
+        const uint8_t* f_codes = a.wp;
+        const uint8_t* f_scales = a.wp;
+        bool f_live = false;
+        auto open_tile = [&]() {  // step over the tiles until f_kb lies in one
+            while (!t.done() && f_kb >= KT) {
+                f_kb -= KT;
+                t.next();
+            }
+            if (t.done()) return;
+            const int u = t.ct * 4 + quarter;
+            f_live = u < NU;
+            const uint8_t* we = a.wp + static_cast<size_t>(t.e) * a.expert_stride;
+            f_codes = we + static_cast<size_t>(u) * KT * kExUnitBytes + lane * 16;
+            f_scales = we + a.scale_offset + static_cast<size_t>(u) * (a.K / a.g) * (kExUnitN * 2) + gc * 8;
+        };
+        auto fetch = [&](int d) {
+            if (t.done()) {
+                valid &= ~(1u << d);
+                return;
+            }
+            valid |= 1u << d;
+            live = f_live ? live | (1u << d) : live & ~(1u << d);
+            if (f_live) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w[d][i] = ldg_stream16(f_codes + static_cast<size_t>(f_kb) * kExUnitBytes + i * 512);
+                if (SL) {
+#pragma unroll
+                    for (int i = 0; i < kS; ++i) {
+                        const int grp = SL == 1 ? f_kb * kTileK / a.g : f_kb * SL + i;
+                        sc[d][i] = __ldg(reinterpret_cast<const uint2*>(f_scales + static_cast<size_t>(grp) * (kExUnitN * 2)));
+                    }
+                }
+            }
+            f_kb += 2;
+            if (f_kb >= KT) open_tile();
+        };
+        open_tile();
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[d][i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < kS; ++i) sc[d][i] = make_uint2(0, 0);
+            fetch(d);
+        }
+        const uint32_t tbase = tmem + kTmemA + (static_cast<uint32_t>(quarter * 32) << 16);
+        unsigned n = 2 * par;  // chunk number of the k-block's first half
+        bool ok = true;
+        while (ok && (valid & 1u)) {
+#pragma unroll
+            for (int d = 0; d < kDepth; ++d) {
+                if (!ok || !((valid >> d) & 1u)) break;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const unsigned c = n + half;
+                    // the chunk four before has left the slot; the first four find it empty
+                    if (c >= kSlotsA) {
+                        const unsigned before = c - kSlotsA;
+                        ok = __all_sync(kFull, wait_phase(&bars.empty[before % kStagesB], (before / kStagesB) & 1, ctl));
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+                    if ((live >> d) & 1u) {
+#pragma unroll
+                        for (int rt = 0; rt < 2; ++rt) {
+                            uint32_t v[16];
+#pragma unroll
+                            for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    const uint4 q4 = w[d][rt * 2 + h];
+                                    uint32_t p[4];
+                                    dequant8(half ? (b ? q4.w : q4.z) : (b ? q4.y : q4.x), p);
+                                    if (SL) {
+                                        const uint2 sv = sc[d][SL == 4 ? (2 * half + b) % kS : SL == 2 ? half % kS : 0];
+                                        const uint32_t pair = rt ? sv.y : sv.x;
+                                        const __half2 s2 = *reinterpret_cast<const __half2*>(&pair);
+                                        const __half2 sb = h ? __high2half2(s2) : __low2half2(s2);
+#pragma unroll
+                                        for (int i = 0; i < 4; ++i) {
+                                            const __half2 m = __hmul2(*reinterpret_cast<__half2*>(&p[i]), sb);
+                                            p[i] = *reinterpret_cast<const uint32_t*>(&m);
+                                        }
+                                    }
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) v[2 * (4 * b + i) + h] = p[i];
+                                }
+                            }
+                            tmem_st_16x128b_x8(tbase + (c % kSlotsA) * (kChunkK / 2) + (static_cast<uint32_t>(rt * 16) << 16), v);
+                        }
+                        tmem_st_wait();
+                        tc_fence_before();
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.full_a[c % kSlotsA]);
+                }
+                n += 4;
+                if (ok) fetch(d);
+            }
+        }
+    } else {
         // ---------------------------------------------------------------- epilogue
         const int quarter = warp & 3;
         const int n_out = a.gated ? a.N / 2 : a.N;
         int buf = 0;
         uint32_t ph = 0;
-        for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-            const TileL t = locate(tile, CT, a.E, s_start, s_tiles);
+        for (; !t.done(); t.next()) {
             const int v = t.ct * kColsL + quarter * 32 + lane;  // layout column of this lane
             float cs = 1.f;
             if (SL == 0 && v < a.N) {
@@ -311,132 +444,13 @@ __global__ void __launch_bounds__(kLThreads, 1) experts_large_kernel(const __gri
             buf ^= 1;
             if (buf == 0) ph ^= 1;
         }
-    } else if (warp >= kDqWarp0) {
-        // ---------------------------------------------------------------- weights
-        const int dw = warp - kDqWarp0;
-        const int q = lane & 3, gc = lane >> 2;
-        constexpr int kS = SL ? SL : 1;
-        uint4 w[kDepth][2];
-        uint32_t sc[kDepth][kS];
-        uint32_t valid = 0, live = 0;  // bit d: slot d holds a k-block / one inside the weight
-        long long f_tile = blockIdx.x;
-        int f_kb = 0;
-        bool f_live = false;
-        const uint8_t* f_codes = a.wp;
-        const uint8_t* f_scales = a.wp;
-        auto open_tile = [&]() {
-            if (f_tile >= tiles) return;
-            const TileL t = locate(f_tile, CT, a.E, s_start, s_tiles);
-            const int u = t.ct * 4 + (dw >> 1);
-            f_live = u < NU;
-            const uint8_t* we = a.wp + static_cast<size_t>(t.e) * a.expert_stride;
-            f_codes = we + static_cast<size_t>(u) * KT * kExUnitBytes + (dw & 1) * 1024 + lane * 16;
-            f_scales = we + a.scale_offset + static_cast<size_t>(u) * (a.K / a.g) * (kExUnitN * 2) + gc * 8 + (dw & 1) * 4;
-        };
-        open_tile();
-        int s = 0;
-        uint32_t ph = 1;
-        bool ok = true;
-        auto fetch = [&](int d) {
-            if (f_tile >= tiles) {
-                valid &= ~(1u << d);
-                return;
-            }
-            valid |= 1u << d;
-            live = f_live ? live | (1u << d) : live & ~(1u << d);
-            if (f_live) {
-                w[d][0] = ldg_stream16(f_codes + static_cast<size_t>(f_kb) * kExUnitBytes);
-                w[d][1] = ldg_stream16(f_codes + static_cast<size_t>(f_kb) * kExUnitBytes + 512);
-                if (SL) {
-#pragma unroll
-                    for (int i = 0; i < kS; ++i) {
-                        const int grp = SL == 1 ? f_kb * kTileK / a.g : f_kb * SL + i;
-                        sc[d][i] = __ldg(reinterpret_cast<const uint32_t*>(f_scales + static_cast<size_t>(grp) * (kExUnitN * 2)));
-                    }
-                }
-            }
-            if (++f_kb == KT) {
-                f_kb = 0;
-                f_tile += gridDim.x;
-                open_tile();
-            }
-        };
-#pragma unroll
-        for (int d = 0; d < kDepth; ++d) {
-            w[d][0] = w[d][1] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int i = 0; i < kS; ++i) sc[d][i] = 0;
-            fetch(d);
-        }
-        while (ok && (valid & 1u)) {
-#pragma unroll
-            for (int d = 0; d < kDepth; ++d) {
-                if (!ok || !((valid >> d) & 1u)) break;
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    ok = __all_sync(kFull, wait_phase(&bars.empty[s], ph, ctl));
-                    if (!ok) break;
-                    if ((live >> d) & 1u) {
-                        uint8_t* row = ring + s * kStageL + (dw * 16 + gc) * 128;
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            // lanes of odd gc take the two 32-row blocks in the other order: a store's
-                            // eight lanes then cover all banks
-                            const uint32_t wa = half ? w[d][h].z : w[d][h].x, wb = half ? w[d][h].w : w[d][h].y;
-                            const bool swap = gc & 1;
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const uint32_t word = (j == 0) != swap ? wa : wb;
-                                const int c = (j == 0) != swap ? 0 : 1;  // 32-row block of the chunk
-                                uint32_t p[4];
-                                dequant8(word, p);
-                                if (SL) {
-                                    // scale of the block's group: slot (2*half + c) * SL / 4
-                                    uint32_t sv;
-                                    if (SL == 4) sv = ((j == 0) != swap) ? sc[d][(2 * half) % kS] : sc[d][(2 * half + 1) % kS];
-                                    else if (SL == 2) sv = sc[d][half % kS];
-                                    else sv = sc[d][0];
-                                    const __half2 s2 = *reinterpret_cast<const __half2*>(&sv);
-                                    const __half2 sb = h ? __high2half2(s2) : __low2half2(s2);
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) {
-                                        const __half2 m = __hmul2(*reinterpret_cast<__half2*>(&p[i]), sb);
-                                        p[i] = *reinterpret_cast<const uint32_t*>(&m);
-                                    }
-                                }
-                                *reinterpret_cast<uint4*>(row + h * 8 * 128 + (((c * 4 + q) ^ gc) << 4)) =
-                                    make_uint4(p[0], p[1], p[2], p[3]);
-                            }
-                        }
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars.full_a[s]);
-                    if (++s == kStagesL) {
-                        s = 0;
-                        ph ^= 1;
-                    }
-                }
-                if (ok) fetch(d);
-            }
-        }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) {
+    if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
-}
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-template <int SL>
-cudaError_t launch_sl(const CUtensorMap& map, const LargeArgs& a, int num_sms, cudaStream_t st) {
-    experts_large_kernel<SL><<<num_sms, kLThreads, kSmemL, st>>>(map, a);
-    return cudaGetLastError();
 }
 
 }  // namespace
@@ -450,25 +464,12 @@ cudaError_t configure_experts_large() {
 }
 
 cudaError_t launch_experts_large(const ExpertArgs& a, const DeviceInfo& d, cudaStream_t st) {
-    // the activations as [rows, K] with boxes of one row x 64 elements: gather4 takes any four rows
-    const long long a_rows = static_cast<long long>(a.pairs) / a.a_div;
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.K), static_cast<cuuint64_t>(a_rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(a.K) * 2};
-    const cuuint32_t box[2] = {kChunkK, 1}, estr[2] = {1, 1};
-    CUtensorMap map;
-    std::memset(&map, 0, sizeof(map));
-    if (reinterpret_cast<EncodeTiledFn>(d.encode)(&map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<uint16_t*>(a.a),
-                                                  dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                                                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return cudaErrorInvalidValue;
-    LargeArgs l;
-    l.e = a;
-    l.timeout_ns = d.timeout_ns;
-    if (a.g == a.K) return launch_sl<0>(map, l, d.num_sms, st);
-    if (a.g == 64) return launch_sl<2>(map, l, d.num_sms, st);
-    if (a.g == 32) return launch_sl<4>(map, l, d.num_sms, st);
-    return launch_sl<1>(map, l, d.num_sms, st);
+    const LargeArgs l{a, d.timeout_ns};
+    if (a.g == a.K) experts_large_kernel<0><<<d.num_sms, kLThreads, kSmemL, st>>>(l);
+    else if (a.g == 64) experts_large_kernel<2><<<d.num_sms, kLThreads, kSmemL, st>>>(l);
+    else if (a.g == 32) experts_large_kernel<4><<<d.num_sms, kLThreads, kSmemL, st>>>(l);
+    else experts_large_kernel<1><<<d.num_sms, kLThreads, kSmemL, st>>>(l);
+    return cudaGetLastError();
 }
 
 }  // namespace wq

@@ -37,21 +37,27 @@ __global__ void __launch_bounds__(kThreads) codes_kernel(uint32_t* __restrict__ 
         const int u = static_cast<int>(unit / KT);
         const int c = cq >> 2, q = cq & 3;
         const int n = source_column(u * kExUnitN + col, N, gated);
-        const long long qrow = static_cast<long long>(kb) * 16 + c * 4 + q;
+        // the block's four words of Q for this column: rows 32c + 8i .. + 7, two of them each
+        uint32_t* src = Q + (e * (K / 8) + static_cast<long long>(kb) * 16 + c * 4) * N + (n < 0 ? 0 : n);
         uint32_t* word = reinterpret_cast<uint32_t*>(wp + e * stride + unit * kExUnitBytes) +
                          (((col >> 3) * 32 + (col & 7) * 4 + q) * 4 + c);
-        uint32_t* src = Q + (e * (K / 8) + qrow) * N + (n < 0 ? 0 : n);
-        uint32_t out = 0;
         if (kUnpack) {
             if (n < 0) continue;
-            const uint32_t in = *word;
+            // this thread writes Q's word i = q, whose codes lie in the words of all four q
+            uint32_t out = 0;
+            const uint32_t* first = word - q * 4;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) out |= ((in >> (4 * nibble_of(j))) & 0xFu) << (4 * j);
-            *src = out;
+            for (int j = 0; j < 8; ++j)
+                out |= ((first[(j >> 1) * 4] >> (4 * nibble_of(2 * q + (j & 1)))) & 0xFu) << (4 * j);
+            src[static_cast<size_t>(q) * N] = out;
         } else {
-            const uint32_t in = n < 0 ? 0x88888888u : *src;
+            uint32_t out = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) out |= ((in >> (4 * j)) & 0xFu) << (4 * nibble_of(j));
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t in = n < 0 ? 0x88888888u : src[static_cast<size_t>(i) * N];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) out |= ((in >> (4 * (2 * q + b))) & 0xFu) << (4 * nibble_of(2 * i + b));
+            }
             *word = out;
         }
     }

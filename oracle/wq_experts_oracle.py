@@ -123,7 +123,7 @@ def prepack_experts(Q, s, g, gated=False):
     """The prepacked buffer (uint8), padding bytes between experts zero.
 
     Word ``((rt*2 + h)*32 + 4*gc + q)*4 + c`` of unit (u, kb) holds column ``32u + 16rt + 8h + gc``,
-    rows ``128kb + 32c + 8q + j``, code j at nibble NIBBLE_POS_W4A16[j]; then the scales."""
+    rows ``128kb + 32c + 8i + 2q + b``, code 2i + b at nibble NIBBLE_POS_W4A16[2i + b]; then the scales."""
     E, K8, N = Q.shape
     K = K8 * 8
     stride = prepacked_bytes_experts(1, K, N, g)
@@ -143,7 +143,7 @@ def prepack_experts(Q, s, g, gated=False):
                 for qq in range(4):
                     at = ((col // 8) * 32 + 4 * (col % 8) + qq) * 4 + c
                     for j in range(8):
-                        v = full[32 * c + 8 * qq + j::TILE_K, col::32]          # [KT, NU]
+                        v = full[32 * c + 8 * (j // 2) + 2 * qq + j % 2::TILE_K, col::32]  # [KT, NU]
                         words[:, :, at] |= v.T << np.uint32(4 * NIBBLE_POS_W4A16[j])
         scales = np.zeros((NU, G, 32), dtype=np.float16)
         for col in range(32):
