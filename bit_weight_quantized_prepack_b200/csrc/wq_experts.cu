@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kThreads) experts_kernel(ExpertArgs a, int sta
             if (r < nrows) {
                 const int p = __ldg(a.rows + row0 + r);
                 if (static_cast<unsigned>(p) < static_cast<unsigned>(a.pairs))
-                    arow[b] = a.a + static_cast<size_t>(p / a.a_div) * a.K + q * 8;
+                    arow[b] = a.a + static_cast<size_t>(row_of_pair(p, a)) * a.K + q * 8;
                 else
                     atomicCAS(a.status, 0, 1 /* WQ_ERR_INVALID_ARG */);
             }

@@ -76,6 +76,7 @@ struct ExpertArgs {
     int* status;               // device status word
     size_t expert_stride, scale_offset;
     int pairs, a_div;          // pair p reads row p / a_div of a
+    unsigned a_mul;            // ceil(2^32 / a_div): the division as a product (row_of_pair)
     int E, N, K, g;
     int gated;
 };

@@ -55,6 +55,7 @@ int run_products(const uint16_t* A, const void* Wp, const int32_t* offsets, cons
     a.scale_offset = ex_scale_offset(K, N);
     a.pairs = T * top_k;
     a.a_div = a_div;
+    a.a_mul = static_cast<unsigned>(((1ull << 32) + a_div - 1) / a_div);  // unused for a_div == 1
     a.E = E;
     a.N = N;
     a.K = K;

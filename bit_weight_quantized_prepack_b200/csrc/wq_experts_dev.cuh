@@ -76,6 +76,13 @@ __device__ void expert_table(const int32_t* offsets, int E, int pairs, int tile_
     __syncthreads();
 }
 
-__device__ __forceinline__ float silu_mul(float gate, float up) { return gate / (1.0f + __expf(-gate)) * up; }
+// p / a_div for 0 <= p < 2^28, a_div <= 32. With m = ceil(2^32 / d) the product's high word is at
+// most one above the quotient (p * m / 2^32 < p / d + 2^-4), which the second term takes back.
+__device__ __forceinline__ int row_of_pair(int p, const ExpertArgs& a) {
+    const int r = static_cast<int>(__umulhi(static_cast<unsigned>(p), a.a_mul));
+    return a.a_div == 1 ? p : r - (r * a.a_div > p);
+}
+
+__device__ __forceinline__ float silu_mul(float gate, float up) { return __fdividef(gate, 1.0f + __expf(-gate)) * up; }
 
 }  // namespace wq

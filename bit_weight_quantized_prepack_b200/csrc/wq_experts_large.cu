@@ -2,16 +2,16 @@
 //
 // Tile: 128 columns of one expert's weight (the MMA's M) x up to 192 of its rows (the MMA's N),
 // all of K in chunks of 64 rows. One persistent CTA per SM, warp-specialised:
-//   warps 0..3   gather the rows' 128-byte pieces with cp.async into a ring of 8 chunks, four
-//                chunks ahead of what they have signalled;
+//   warps 0..2   gather the rows' 128-byte pieces with cp.async into a ring of 8 chunks; a chunk's
+//                barrier is completed by the copies themselves;
+//   warp 3       one elected thread issues the MMAs: weights from tensor memory, rows from shared
+//                memory (128-byte swizzle), fp32 sums in tensor memory, two accumulators of 192
+//                columns used in turn;
 //   warps 4..7   epilogue of the tile before, while the next one is multiplied;
 //   warps 8..15  dequantise: warp 8 + w takes the tile's columns 32 (w % 4) .. + 31 of every second
 //                k-block, loads its codes straight from global memory several k-blocks ahead
 //                (across tiles) and stores fp16 weights (q - 8) * s, rounded once, into one of
-//                four 64-row slots in tensor memory;
-//   warp 16      one elected thread issues the MMAs: weights from tensor memory, rows from shared
-//                memory (128-byte swizzle), fp32 sums in tensor memory, two accumulators of 192
-//                columns used in turn.
+//                four 64-row slots in tensor memory.
 // An expert's rows are split evenly over its row tiles. Tiles of the same rows are neighbours, so
 // that the rows are gathered from L2 after the first time.
 // Why so: the weight operand in tensor memory saves the ~32 cycles that each MMA spends on loading
@@ -30,18 +30,20 @@ namespace wq {
 
 namespace {
 
-constexpr int kLThreads = 17 * 32;
+constexpr int kLThreads = 16 * 32;
 constexpr int kRowsMax = 192;                      // rows of a tile
 constexpr int kColsL = 128;                        // columns of a tile
 constexpr int kChunkK = 64;                        // weight rows of a stage: one 128-byte swizzle span
 constexpr int kBBytes = kRowsMax * kChunkK * 2;    // 24 KiB
 constexpr int kStagesB = 8;
 constexpr int kSlotsA = 4;
-constexpr int kLag = 4;                            // chunks issued after the one that is signalled
 constexpr int kTmemA = 2 * kRowsMax;               // tensor-memory column of the weight slots
 constexpr int kSmemL = kStagesB * kBBytes + 1024;  // + alignment of the first stage
-constexpr int kGatherWarps = 4, kEpiWarp0 = 4, kDqWarp0 = 8, kMmaWarp = 16;
-constexpr int kDepth = 3;                          // k-blocks of codes in flight per dequant warp
+constexpr int kGatherWarps = 3, kMmaWarp = 3, kEpiWarp0 = 4, kDqWarp0 = 8;
+constexpr int kQuads = kRowsMax / 4 / kGatherWarps;  // 4-row pieces of a chunk per gather warp
+
+constexpr int kYRow = 80, kYRowGated = 48;         // bytes of an output row on its way out, with padding
+constexpr int kYBytes = 32 * kYRow;
 
 struct Bars {
     uint64_t full_a[kSlotsA], full_b[kStagesB], empty[kStagesB];
@@ -162,6 +164,7 @@ __global__ void __launch_bounds__(kLThreads, 1) experts_large_kernel(LargeArgs a
     extern __shared__ uint8_t smem_raw[];
     __shared__ Bars bars;
     __shared__ int s_start[kExMaxExperts + 1], s_tiles[kExMaxExperts + 1], s_scratch[kLThreads / 32];
+    __shared__ __align__(16) uint8_t stage_y[4 * kYBytes];
     __shared__ uint32_t s_tmem;
     __shared__ int s_stop;
     const ExpertArgs& a = args.e;
@@ -171,7 +174,7 @@ __global__ void __launch_bounds__(kLThreads, 1) experts_large_kernel(LargeArgs a
     if (tid == 0) {
         for (int i = 0; i < kSlotsA; ++i) mbar_init(&bars.full_a[i], 4);
         for (int i = 0; i < kStagesB; ++i) {
-            mbar_init(&bars.full_b[i], kGatherWarps);
+            mbar_init(&bars.full_b[i], kGatherWarps * 32);
             mbar_init(&bars.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -198,49 +201,59 @@ __global__ void __launch_bounds__(kLThreads, 1) experts_large_kernel(LargeArgs a
 
     if (warp < kGatherWarps) {
         // ---------------------------------------------------------------- rows of the activations
-        // thread (warp, lane): 16-byte piece lane % 8 of rows 16j + 4 warp + lane / 8
-        const int piece = lane & 7, r0 = warp * 4 + (lane >> 3);
-        const uint32_t dst0 = smem_addr(ring) + r0 * 128 + ((piece ^ (r0 & 7)) << 4);
+        // thread (warp, lane): 16-byte piece lane % 8 of rows 4 (3j + warp) + lane / 8
+        const int piece = lane & 7, sub = lane >> 3;
+        // place of the piece in the swizzled row, for quads that begin an 8-row group and others
+        const uint32_t base = smem_addr(ring) + (warp * 4 + sub) * 128;
+        const uint32_t dst_even = base + ((piece ^ (((warp & 1) * 4 + sub) & 7)) << 4);
+        const uint32_t dst_odd = base + ((piece ^ ((((warp + 1) & 1) * 4 + sub) & 7)) << 4);
         unsigned n = 0;  // chunks issued
         bool ok = true;
-        for (; ok && !t.done(); t.next()) {
-            const uint16_t* src[kRowsMax / 16];
+        int place[kQuads];  // the next tile's entries of the lists, read while this one is copied
+        int have = 0;       // rows of that tile
+        auto read_rows = [&]() {
+            have = t.done() ? 0 : t.nrows;
 #pragma unroll
-            for (int j = 0; j < kRowsMax / 16; ++j) {
-                // places behind the tile's last row keep what was there: their sums are never stored
+            for (int j = 0; j < kQuads; ++j) {
+                const int r = (j * kGatherWarps + warp) * 4 + sub;
+                place[j] = r < have ? __ldg(a.rows + t.row0 + r) : -1;
+            }
+        };
+        read_rows();
+        bool more = !t.done();
+        while (ok && more) {
+            const uint16_t* src[kQuads];
+#pragma unroll
+            for (int j = 0; j < kQuads; ++j) {
+                // rows behind the tile's last keep what was there: their sums are never stored
                 src[j] = nullptr;
-                if (j * 16 + r0 < t.nrows) {
-                    const int p = __ldg(a.rows + t.row0 + j * 16 + r0);
-                    if (static_cast<unsigned>(p) < static_cast<unsigned>(a.pairs))
-                        src[j] = a.a + static_cast<size_t>(p / a.a_div) * a.K + piece * 8;
-                    else
-                        atomicCAS(a.status, 0, 1 /* WQ_ERR_INVALID_ARG */);
-                }
+                if (static_cast<unsigned>(place[j]) < static_cast<unsigned>(a.pairs))
+                    src[j] = a.a + static_cast<size_t>(row_of_pair(place[j], a)) * a.K + piece * 8;
+                else if ((j * kGatherWarps + warp) * 4 + sub < have)
+                    atomicCAS(a.status, 0, 1 /* WQ_ERR_INVALID_ARG */);
             }
             for (int c = 0; c < chunks; ++c, ++n) {
                 ok = __all_sync(kFull, wait_phase(&bars.empty[n % kStagesB], ((n / kStagesB) & 1) ^ 1, ctl));
                 if (!ok) break;
-                const uint32_t dst = dst0 + (n % kStagesB) * kBBytes;
+                const uint32_t stage = (n % kStagesB) * kBBytes;
 #pragma unroll
-                for (int j = 0; j < kRowsMax / 16; ++j)
+                for (int j = 0; j < kQuads; ++j)
                     if (src[j])
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + j * 2048),
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                         ((j & 1) ? dst_odd : dst_even) + stage + j * (kGatherWarps * 512)),
                                      "l"(src[j] + c * kChunkK)
                                      : "memory");
-                asm volatile("cp.async.commit_group;" ::: "memory");
-                if (n >= kLag) {
-                    asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars.full_b[(n - kLag) % kStagesB]);
+                if (c == 1) {
+                    t.next();
+                    more = !t.done();
+                    read_rows();
                 }
+                // arrives when this thread's copies have landed; the MMA's thread orders the proxies
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&bars.full_b[n % kStagesB]))
+                             : "memory");
             }
         }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0)
-            for (unsigned i = n > kLag ? n - kLag : 0; i < n; ++i) mbar_arrive(&bars.full_b[i % kStagesB]);
+        asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------------- MMAs
         // One elected thread runs the whole loop: inside its branch the operands stay uniform (174
@@ -251,7 +264,8 @@ __global__ void __launch_bounds__(kLThreads, 1) experts_large_kernel(LargeArgs a
             uint32_t aph = 1;
             bool ok = true;
             const uint64_t desc0 = smem_desc_sw128(smem_addr(ring));
-            for (; ok && !t.done(); t.next()) {
+            bool more = !t.done();
+            while (ok && more) {
                 const uint32_t idesc = idesc_f16_f32(kColsL, (t.nrows + 15) / 16 * 16);
                 const uint32_t d = tmem + buf * kRowsMax;
                 ok = wait_phase(&bars.acc_empty[buf], aph, ctl);
@@ -261,12 +275,17 @@ __global__ void __launch_bounds__(kLThreads, 1) experts_large_kernel(LargeArgs a
                          wait_phase(&bars.full_a[n % kSlotsA], (n / kSlotsA) & 1, ctl);
                     if (!ok) break;
                     tc_fence_after();
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the rows came by cp.async
                     const uint64_t db = smem_desc_advance(desc0, (n % kStagesB) * kBBytes);
                     const uint32_t wa = tmem + kTmemA + (n % kSlotsA) * (kChunkK / 2);
 #pragma unroll
                     for (int k = 0; k < kChunkK / 16; ++k)
                         mma_f16_ts(d, wa + k * 8, smem_desc_advance(db, k * 32), idesc, (c | k) ? 1u : 0u);
                     tc_commit(&bars.empty[n % kStagesB]);
+                    if (c == 0) {  // the next tile is found while this one is multiplied
+                        t.next();
+                        more = !t.done();
+                    }
                 }
                 if (ok) tc_commit(&bars.acc_full[buf]);
                 buf ^= 1;
@@ -282,6 +301,7 @@ __global__ void __launch_bounds__(kLThreads, 1) experts_large_kernel(LargeArgs a
         const int quarter = warp & 3, par = (warp - kDqWarp0) >> 2;
         const int gc = lane >> 2;
         constexpr int kS = SL ? SL : 1;
+        constexpr int kDepth = SL == 4 ? 2 : 3;  // k-blocks of codes in flight
         uint4 w[kDepth][4];    // [(rt, h)]
         uint2 sc[kDepth][kS];  // scales of the columns (rt, h) as fp16
         uint32_t valid = 0, live = 0;  // bit d: slot d holds a k-block / one inside the weight
@@ -342,6 +362,30 @@ __global__ void __launch_bounds__(kLThreads, 1) experts_large_kernel(LargeArgs a
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     const unsigned c = n + half;
+                    uint32_t v[2][16];
+#pragma unroll
+                    for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+                        for (int b = 0; b < 2; ++b)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const uint4 q4 = w[d][rt * 2 + h];
+                                uint32_t p[4];
+                                dequant8(half ? (b ? q4.w : q4.z) : (b ? q4.y : q4.x), p);
+                                if (SL) {
+                                    const uint2 sv = sc[d][SL == 4 ? (2 * half + b) % kS : SL == 2 ? half % kS : 0];
+                                    const uint32_t pair = rt ? sv.y : sv.x;
+                                    const __half2 s2 = *reinterpret_cast<const __half2*>(&pair);
+                                    const __half2 sb = h ? __high2half2(s2) : __low2half2(s2);
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        const __half2 m = __hmul2(*reinterpret_cast<__half2*>(&p[i]), sb);
+                                        p[i] = *reinterpret_cast<const uint32_t*>(&m);
+                                    }
+                                }
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) v[rt][2 * (4 * b + i) + h] = p[i];
+                            }
                     // the chunk four before has left the slot; the first four find it empty
                     if (c >= kSlotsA) {
                         const unsigned before = c - kSlotsA;
@@ -350,33 +394,9 @@ __global__ void __launch_bounds__(kLThreads, 1) experts_large_kernel(LargeArgs a
                         tc_fence_after();
                     }
                     if ((live >> d) & 1u) {
-#pragma unroll
-                        for (int rt = 0; rt < 2; ++rt) {
-                            uint32_t v[16];
-#pragma unroll
-                            for (int b = 0; b < 2; ++b) {
-#pragma unroll
-                                for (int h = 0; h < 2; ++h) {
-                                    const uint4 q4 = w[d][rt * 2 + h];
-                                    uint32_t p[4];
-                                    dequant8(half ? (b ? q4.w : q4.z) : (b ? q4.y : q4.x), p);
-                                    if (SL) {
-                                        const uint2 sv = sc[d][SL == 4 ? (2 * half + b) % kS : SL == 2 ? half % kS : 0];
-                                        const uint32_t pair = rt ? sv.y : sv.x;
-                                        const __half2 s2 = *reinterpret_cast<const __half2*>(&pair);
-                                        const __half2 sb = h ? __high2half2(s2) : __low2half2(s2);
-#pragma unroll
-                                        for (int i = 0; i < 4; ++i) {
-                                            const __half2 m = __hmul2(*reinterpret_cast<__half2*>(&p[i]), sb);
-                                            p[i] = *reinterpret_cast<const uint32_t*>(&m);
-                                        }
-                                    }
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) v[2 * (4 * b + i) + h] = p[i];
-                                }
-                            }
-                            tmem_st_16x128b_x8(tbase + (c % kSlotsA) * (kChunkK / 2) + (static_cast<uint32_t>(rt * 16) << 16), v);
-                        }
+                        const uint32_t slot = tbase + (c % kSlotsA) * (kChunkK / 2);
+                        tmem_st_16x128b_x8(slot, v[0]);
+                        tmem_st_16x128b_x8(slot + (16u << 16), v[1]);
                         tmem_st_wait();
                         tc_fence_before();
                     }
@@ -406,35 +426,49 @@ __global__ void __launch_bounds__(kLThreads, 1) experts_large_kernel(LargeArgs a
             if (!__all_sync(kFull, wait_phase(&bars.acc_full[buf], ph, ctl))) break;
             tc_fence_after();
             const uint32_t taddr = tmem + buf * kRowsMax + (static_cast<uint32_t>(quarter * 32) << 16);
+            uint8_t* out = stage_y + quarter * kYBytes;
             for (int m0 = 0; m0 < t.nrows; m0 += 32) {
                 uint32_t d[32];
                 tmem_ld_x32(taddr + m0, d);
                 const int pair = static_cast<unsigned>(pair_next) < static_cast<unsigned>(a.pairs) ? pair_next : -1;
                 pair_next = m0 + 32 + lane < t.nrows ? __ldg(a.rows + t.row0 + m0 + 32 + lane) : -1;
                 tmem_ld_wait();
+                // 32 rows x this warp's columns turned round in shared memory: rows of 64 (gated: 32)
+                // bytes, so that a row leaves in 16-byte stores
+                __syncwarp();
+                if (a.gated) {
+                    // gate lanes take the first 16 rows, up lanes the others
+                    const bool up = lane & 8;
+                    uint16_t* col = reinterpret_cast<uint16_t*>(out) + ((lane >> 4) * 8 + (lane & 7)) + (up ? 16 * (kYRowGated / 2) : 0);
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    float x0 = __uint_as_float(d[i]), x1 = __uint_as_float(d[i + 1]);
-                    if (SL == 0) {
-                        x0 *= cs;
-                        x1 *= cs;
-                    }
-                    if (a.gated) {
-                        // gate lanes take row i, up lanes row i + 1
-                        const bool up = lane & 8;
+                    for (int i = 0; i < 16; ++i) {
+                        const float x0 = __uint_as_float(d[i]) * cs, x1 = __uint_as_float(d[i + 16]) * cs;
                         const float other = __shfl_xor_sync(kFull, up ? x0 : x1, 8);
                         const float h = up ? silu_mul(other, x1) : silu_mul(x0, other);
-                        const int p = __shfl_sync(kFull, pair, i + (up ? 1 : 0));
-                        const int n = (v >> 4) * 8 + (v & 7);
-                        if (p >= 0 && v < a.N) a.y[static_cast<size_t>(p) * n_out + n] = __half_as_ushort(__float2half_rn(h));
-                    } else {
-                        // even lanes take row i of two neighbouring columns, odd lanes row i + 1
-                        const bool odd = lane & 1;
-                        const float other = __shfl_xor_sync(kFull, odd ? x0 : x1, 1);
-                        const __half2 h = odd ? __floats2half2_rn(other, x1) : __floats2half2_rn(x0, other);
-                        const int p = __shfl_sync(kFull, pair, i + (odd ? 1 : 0));
-                        const int n = v & ~1;
-                        if (p >= 0 && n < a.N) *reinterpret_cast<__half2*>(a.y + static_cast<size_t>(p) * n_out + n) = h;
+                        col[i * (kYRowGated / 2)] = __half_as_ushort(__float2half_rn(h));
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int m = i * 16 + (lane >> 1);
+                        const int p = __shfl_sync(kFull, pair, m);
+                        const int n = t.ct * (kColsL / 2) + quarter * 16 + (lane & 1) * 8;
+                        const uint4 v4 = *reinterpret_cast<const uint4*>(out + m * kYRowGated + (lane & 1) * 16);
+                        if (p >= 0 && n < n_out) *reinterpret_cast<uint4*>(a.y + static_cast<size_t>(p) * n_out + n) = v4;
+                    }
+                } else {
+                    uint16_t* col = reinterpret_cast<uint16_t*>(out) + lane;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        col[i * (kYRow / 2)] = __half_as_ushort(__float2half_rn(__uint_as_float(d[i]) * cs));
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int m = i * 8 + (lane >> 2);
+                        const int p = __shfl_sync(kFull, pair, m);
+                        const int n = t.ct * kColsL + quarter * 32 + (lane & 3) * 8;
+                        const uint4 v4 = *reinterpret_cast<const uint4*>(out + m * kYRow + (lane & 3) * 16);
+                        if (p >= 0 && n < n_out) *reinterpret_cast<uint4*>(a.y + static_cast<size_t>(p) * n_out + n) = v4;
                     }
                 }
             }
