@@ -2,8 +2,8 @@
 //
 // Tile: 128 columns of one expert's weight (the MMA's M) x up to 192 of its rows (the MMA's N),
 // all of K in chunks of 64 rows. One persistent CTA per SM, warp-specialised:
-//   warps 0..2   gather the rows' 128-byte pieces with cp.async into a ring of 8 chunks; a chunk's
-//                barrier is completed by the copies themselves;
+//   warps 0..2   gather the rows' 128-byte pieces with cp.async into a ring of 16 chunks, each
+//                warp every third chunk;
 //   warp 3       one elected thread issues the MMAs: weights from tensor memory, rows from shared
 //                memory (128-byte swizzle), fp32 sums in tensor memory, two accumulators of 192
 //                columns used in turn;
@@ -34,19 +34,20 @@ constexpr int kLThreads = 16 * 32;
 constexpr int kRowsMax = 192;                      // rows of a tile
 constexpr int kColsL = 128;                        // columns of a tile
 constexpr int kChunkK = 64;                        // weight rows of a stage: one 128-byte swizzle span
-constexpr int kBBytes = kRowsMax * kChunkK * 2;    // 24 KiB
-constexpr int kStagesB = 8;
+constexpr int kHalfRows = kRowsMax / 2;            // rows of a tile that one CTA of the pair holds
+constexpr int kBBytes = kHalfRows * kChunkK * 2;   // 12 KiB
+constexpr int kStagesB = 16;
 constexpr int kSlotsA = 4;
 constexpr int kTmemA = 2 * kRowsMax;               // tensor-memory column of the weight slots
 constexpr int kSmemL = kStagesB * kBBytes + 1024;  // + alignment of the first stage
 constexpr int kGatherWarps = 3, kMmaWarp = 3, kEpiWarp0 = 4, kDqWarp0 = 8;
-constexpr int kQuads = kRowsMax / 4 / kGatherWarps;  // 4-row pieces of a chunk per gather warp
+constexpr int kQuads = kHalfRows / 4;              // a warp's copy instruction takes four rows
 
 constexpr int kYRow = 80, kYRowGated = 48;         // bytes of an output row on its way out, with padding
 constexpr int kYBytes = 32 * kYRow;
 
 struct Bars {
-    uint64_t full_a[kSlotsA], full_b[kStagesB], empty[kStagesB];
+    uint64_t full[kStagesB], empty[kStagesB];
     uint64_t acc_full[2], acc_empty[2], drain;
 };
 
@@ -61,6 +62,25 @@ struct Ctl {
     unsigned long long timeout_ns;
 };
 
+// Arrive on the leader's barrier that lies where `bar` lies in this CTA. What the leader's MMAs
+// read is ordered by the proxy and tcgen05 fences before it, not by this arrival: one that releases
+// at cluster scope costs its thread some hundred cycles (up_prefill 366 us against 213).
+__device__ __forceinline__ void mbar_arrive_leader(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .b32 remote;\n\t"
+        "mapa.shared::cluster.u32 remote, %0, 0;\n\t"
+        "mbarrier.arrive.shared::cluster.b64 _, [remote];\n\t}" ::"r"(smem_addr(bar))
+        : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
 // Bounded wait for a phase; false when it expired or another role gave up.
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, const Ctl& c, bool honour_stop = true) {
     if (mbar_test_wait(bar, parity)) return true;
@@ -74,6 +94,34 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, const
             return false;
         }
     }
+}
+
+// Tensor memory, MMA and commit of a CTA pair: the leader's thread multiplies for both CTAs, each
+// with its own 128 weight columns in its tensor memory and half of the rows in its shared memory.
+__device__ __forceinline__ void tmem_alloc2(uint32_t* smem_result, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(smem_result)), "r"(ncols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void mma2_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrive on this barrier of both CTAs when every MMA issued before has completed.
+__device__ __forceinline__ void tc_commit2(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_addr(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -114,8 +162,8 @@ __device__ __forceinline__ uint4 ldg_stream16(const void* p) {
     return v;
 }
 
-// Walk of a CTA over the tiles: row tile rt_all of all experts' row tiles, column tile ct; column
-// tiles of one row tile are neighbours. CTA b takes tiles b, b + grid, ...
+// Walk of a CTA pair over the tiles: row tile rt_all of all experts' row tiles, column tile ct (256
+// columns); column tiles of one row tile are neighbours. Pair b takes tiles b, b + pairs, ...
 struct Walk {
     int rt_all, ct, e;       // position
     int row0, nrows;         // rows of the tile: places row0 .. of the lists
@@ -125,7 +173,7 @@ struct Walk {
 
     __device__ __forceinline__ Walk(int CT_, int E_, const int* s_start, const int* s_tiles)
         : e(0), row0(0), nrows(0), CT(CT_), E(E_), start(s_start), tiles(s_tiles) {
-        const unsigned grid = gridDim.x, b = blockIdx.x;
+        const unsigned grid = gridDim.x / 2, b = blockIdx.x / 2;
         step_rt = grid / CT;
         step_ct = grid % CT;
         rt_all = b / CT;
@@ -160,7 +208,7 @@ struct Walk {
 
 // SL as in the small kernel: scales per k-block and column; 0: per-column, applied in the epilogue.
 template <int SL>
-__global__ void __launch_bounds__(kLThreads, 1) experts_large_kernel(LargeArgs args) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) experts_large_kernel(LargeArgs args) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ Bars bars;
     __shared__ int s_start[kExMaxExperts + 1], s_tiles[kExMaxExperts + 1], s_scratch[kLThreads / 32];
@@ -169,130 +217,149 @@ __global__ void __launch_bounds__(kLThreads, 1) experts_large_kernel(LargeArgs a
     __shared__ int s_stop;
     const ExpertArgs& a = args.e;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = cluster_rank();  // 0: the leader, whose thread issues the pair's MMAs
     uint8_t* ring = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
 
     if (tid == 0) {
-        for (int i = 0; i < kSlotsA; ++i) mbar_init(&bars.full_a[i], 4);
         for (int i = 0; i < kStagesB; ++i) {
-            mbar_init(&bars.full_b[i], kGatherWarps * 32);
+            mbar_init(&bars.full[i], 2 + 8);  // a gather warp and four dequant warps of each CTA
             mbar_init(&bars.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.acc_full[i], 1);
-            mbar_init(&bars.acc_empty[i], 4);
+            mbar_init(&bars.acc_empty[i], 8);
         }
         mbar_init(&bars.drain, 1);
         s_stop = 0;
         fence_barrier_init();
     }
-    if (warp == kMmaWarp) {
-        tmem_alloc(&s_tmem, 512);
-        tmem_relinquish();
-    }
+    if (warp == kMmaWarp) tmem_alloc2(&s_tmem, 512);
     expert_table<kLThreads>(a.offsets, a.E, a.pairs, kRowsMax, s_start, s_tiles, s_scratch);
     tc_fence_before();
     __syncthreads();
+    cluster_sync();  // the barriers of both CTAs stand
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     const Ctl ctl{&s_stop, a.status, args.timeout_ns};
     const int KT = a.K / kTileK, chunks = a.K / kChunkK;
-    const int CT = (a.N + kColsL - 1) / kColsL, NU = ex_units(a.N);
+    const int CT = (a.N + 2 * kColsL - 1) / (2 * kColsL), NU = ex_units(a.N);
     Walk t(CT, a.E, s_start, s_tiles);
 
     if (warp < kGatherWarps) {
         // ---------------------------------------------------------------- rows of the activations
-        // thread (warp, lane): 16-byte piece lane % 8 of rows 4 (3j + warp) + lane / 8
+        // Warp w copies chunks w, w + 3, ... whole: lane l the 16-byte piece l % 8 of rows 4j + l / 8.
+        // It signals a chunk when the next of its own is under way.
         const int piece = lane & 7, sub = lane >> 3;
-        // place of the piece in the swizzled row, for quads that begin an 8-row group and others
-        const uint32_t base = smem_addr(ring) + (warp * 4 + sub) * 128;
-        const uint32_t dst_even = base + ((piece ^ (((warp & 1) * 4 + sub) & 7)) << 4);
-        const uint32_t dst_odd = base + ((piece ^ ((((warp + 1) & 1) * 4 + sub) & 7)) << 4);
-        unsigned n = 0;  // chunks issued
-        bool ok = true;
+        // place of the piece in the swizzled row, for even and odd quads
+        const uint32_t base = smem_addr(ring) + sub * 128;
+        const uint32_t dst_even = base + ((piece ^ sub) << 4), dst_odd = base + ((piece ^ (4 + sub)) << 4);
+        const unsigned row_bytes = static_cast<unsigned>(a.K) * 2;
+        unsigned n = 0;     // chunk
+        bool ok = true, pending = false;
+        unsigned last = 0;  // stage of the pending chunk
+        auto signal = [&]() {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive_leader(&bars.full[last]);
+        };
         int place[kQuads];  // the next tile's entries of the lists, read while this one is copied
-        int have = 0;       // rows of that tile
+        int have = 0;       // rows of that tile that this CTA holds
         auto read_rows = [&]() {
-            have = t.done() ? 0 : t.nrows;
+            const int half = t.done() ? 0 : (t.nrows + 15) / 16 * 8, first = rank * half;
+            have = t.done() ? 0 : min(half, t.nrows - first);
 #pragma unroll
-            for (int j = 0; j < kQuads; ++j) {
-                const int r = (j * kGatherWarps + warp) * 4 + sub;
-                place[j] = r < have ? __ldg(a.rows + t.row0 + r) : -1;
-            }
+            for (int j = 0; j < kQuads; ++j) place[j] = j * 4 + sub < have ? __ldg(a.rows + t.row0 + first + j * 4 + sub) : -1;
         };
         read_rows();
         bool more = !t.done();
         while (ok && more) {
-            const uint16_t* src[kQuads];
+            int row[kQuads];
 #pragma unroll
             for (int j = 0; j < kQuads; ++j) {
                 // rows behind the tile's last keep what was there: their sums are never stored
-                src[j] = nullptr;
-                if (static_cast<unsigned>(place[j]) < static_cast<unsigned>(a.pairs))
-                    src[j] = a.a + static_cast<size_t>(row_of_pair(place[j], a)) * a.K + piece * 8;
-                else if ((j * kGatherWarps + warp) * 4 + sub < have)
-                    atomicCAS(a.status, 0, 1 /* WQ_ERR_INVALID_ARG */);
+                row[j] = -1;
+                if (static_cast<unsigned>(place[j]) < static_cast<unsigned>(a.pairs)) row[j] = row_of_pair(place[j], a);
+                else if (j * 4 + sub < have) atomicCAS(a.status, 0, 1 /* WQ_ERR_INVALID_ARG */);
             }
-            for (int c = 0; c < chunks; ++c, ++n) {
-                ok = __all_sync(kFull, wait_phase(&bars.empty[n % kStagesB], ((n / kStagesB) & 1) ^ 1, ctl));
+            const unsigned tile_n = n;
+            t.next();
+            more = !t.done();
+            bool read = false;
+            // this warp's first chunk of the tile
+            for (int c = (warp + kGatherWarps - tile_n % kGatherWarps) % kGatherWarps; c < chunks; c += kGatherWarps) {
+                n = tile_n + c;
+                const unsigned stage = n % kStagesB;
+                ok = __all_sync(kFull, wait_phase(&bars.empty[stage], ((n / kStagesB) & 1) ^ 1, ctl));
                 if (!ok) break;
-                const uint32_t stage = (n % kStagesB) * kBBytes;
+                const uint8_t* src = reinterpret_cast<const uint8_t*>(a.a + c * kChunkK + piece * 8);
 #pragma unroll
                 for (int j = 0; j < kQuads; ++j)
-                    if (src[j])
+                    if (row[j] >= 0)
                         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                                         ((j & 1) ? dst_odd : dst_even) + stage + j * (kGatherWarps * 512)),
-                                     "l"(src[j] + c * kChunkK)
+                                         ((j & 1) ? dst_odd : dst_even) + stage * kBBytes + j * 512),
+                                     "l"(src + static_cast<unsigned long long>(static_cast<unsigned>(row[j])) * row_bytes)
                                      : "memory");
-                if (c == 1) {
-                    t.next();
-                    more = !t.done();
-                    read_rows();
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                if (pending) {
+                    asm volatile("cp.async.wait_group 1;" ::: "memory");
+                    signal();
                 }
-                // arrives when this thread's copies have landed; the MMA's thread orders the proxies
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&bars.full_b[n % kStagesB]))
-                             : "memory");
+                pending = true;
+                last = stage;
+                if (!read) {
+                    read_rows();
+                    read = true;
+                }
             }
+            if (!read) read_rows();
+            n = tile_n + chunks;
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
+        if (pending) signal();
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------------- MMAs
         // One elected thread runs the whole loop: inside its branch the operands stay uniform (174
         // cycles per MMA from a thread picked by its number, 40 from an elected one).
-        if (elect_one()) {
-            unsigned n = 0;
+        if (rank == 0 && elect_one()) {
+            // The thread's own instructions set the pace of small steps: one barrier per chunk, looked
+            // at while the chunk before is issued, and addresses that only advance.
+            uint32_t stage = 0, ph = 0, aph = 1;
             int buf = 0;
-            uint32_t aph = 1;
             bool ok = true;
             const uint64_t desc0 = smem_desc_sw128(smem_addr(ring));
             bool more = !t.done();
+            bool ready = mbar_test_wait(&bars.full[0], 0);
             while (ok && more) {
-                const uint32_t idesc = idesc_f16_f32(kColsL, (t.nrows + 15) / 16 * 16);
+                const uint32_t idesc = idesc_f16_f32(2 * kColsL, (t.nrows + 15) / 16 * 16);
                 const uint32_t d = tmem + buf * kRowsMax;
                 ok = wait_phase(&bars.acc_empty[buf], aph, ctl);
                 tc_fence_after();
-                for (int c = 0; c < chunks && ok; ++c, ++n) {
-                    ok = wait_phase(&bars.full_b[n % kStagesB], (n / kStagesB) & 1, ctl) &&
-                         wait_phase(&bars.full_a[n % kSlotsA], (n / kSlotsA) & 1, ctl);
-                    if (!ok) break;
+                for (int c = 0; c < chunks; ++c) {
+                    if (!ready) {
+                        ok = wait_phase(&bars.full[stage], ph, ctl);
+                        if (!ok) break;
+                    }
                     tc_fence_after();
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the rows came by cp.async
-                    const uint64_t db = smem_desc_advance(desc0, (n % kStagesB) * kBBytes);
-                    const uint32_t wa = tmem + kTmemA + (n % kSlotsA) * (kChunkK / 2);
+                    const uint64_t db = smem_desc_advance(desc0, stage * kBBytes);
+                    const uint32_t wa = tmem + kTmemA + (stage % kSlotsA) * (kChunkK / 2);
 #pragma unroll
                     for (int k = 0; k < kChunkK / 16; ++k)
-                        mma_f16_ts(d, wa + k * 8, smem_desc_advance(db, k * 32), idesc, (c | k) ? 1u : 0u);
-                    tc_commit(&bars.empty[n % kStagesB]);
+                        mma2_f16_ts(d, wa + k * 8, smem_desc_advance(db, k * 32), idesc, (c | k) ? 1u : 0u);
+                    tc_commit2(&bars.empty[stage]);
+                    stage = (stage + 1) % kStagesB;
+                    ph ^= stage == 0;
+                    ready = mbar_test_wait(&bars.full[stage], ph);
                     if (c == 0) {  // the next tile is found while this one is multiplied
                         t.next();
                         more = !t.done();
                     }
                 }
-                if (ok) tc_commit(&bars.acc_full[buf]);
+                if (ok) tc_commit2(&bars.acc_full[buf]);
                 buf ^= 1;
                 if (buf == 0) aph ^= 1;
             }
             // every MMA done before the CTA frees its tensor memory
-            tc_commit(&bars.drain);
+            tc_commit2(&bars.drain);
             wait_phase(&bars.drain, 0, ctl, false);
         }
         __syncwarp();
@@ -315,7 +382,7 @@ __global__ void __launch_bounds__(kLThreads, 1) experts_large_kernel(LargeArgs a
                 t.next();
             }
             if (t.done()) return;
-            const int u = t.ct * 4 + quarter;
+            const int u = (t.ct * 2 + rank) * 4 + quarter;
             f_live = u < NU;
             const uint8_t* we = a.wp + static_cast<size_t>(t.e) * a.expert_stride;
             f_codes = we + static_cast<size_t>(u) * KT * kExUnitBytes + lane * 16;
@@ -401,7 +468,7 @@ __global__ void __launch_bounds__(kLThreads, 1) experts_large_kernel(LargeArgs a
                         tc_fence_before();
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars.full_a[c % kSlotsA]);
+                    if (lane == 0) mbar_arrive_leader(&bars.full[c % kStagesB]);
                 }
                 n += 4;
                 if (ok) fetch(d);
@@ -414,7 +481,8 @@ __global__ void __launch_bounds__(kLThreads, 1) experts_large_kernel(LargeArgs a
         int buf = 0;
         uint32_t ph = 0;
         for (; !t.done(); t.next()) {
-            const int v = t.ct * kColsL + quarter * 32 + lane;  // layout column of this lane
+            const int ct = t.ct * 2 + rank;
+            const int v = ct * kColsL + quarter * 32 + lane;  // layout column of this lane
             float cs = 1.f;
             if (SL == 0 && v < a.N) {
                 const __half* sp = reinterpret_cast<const __half*>(a.wp + static_cast<size_t>(t.e) * a.expert_stride +
@@ -452,7 +520,7 @@ __global__ void __launch_bounds__(kLThreads, 1) experts_large_kernel(LargeArgs a
                     for (int i = 0; i < 2; ++i) {
                         const int m = i * 16 + (lane >> 1);
                         const int p = __shfl_sync(kFull, pair, m);
-                        const int n = t.ct * (kColsL / 2) + quarter * 16 + (lane & 1) * 8;
+                        const int n = ct * (kColsL / 2) + quarter * 16 + (lane & 1) * 8;
                         const uint4 v4 = *reinterpret_cast<const uint4*>(out + m * kYRowGated + (lane & 1) * 16);
                         if (p >= 0 && n < n_out) *reinterpret_cast<uint4*>(a.y + static_cast<size_t>(p) * n_out + n) = v4;
                     }
@@ -466,7 +534,7 @@ __global__ void __launch_bounds__(kLThreads, 1) experts_large_kernel(LargeArgs a
                     for (int i = 0; i < 4; ++i) {
                         const int m = i * 8 + (lane >> 2);
                         const int p = __shfl_sync(kFull, pair, m);
-                        const int n = t.ct * kColsL + quarter * 32 + (lane & 3) * 8;
+                        const int n = ct * kColsL + quarter * 32 + (lane & 3) * 8;
                         const uint4 v4 = *reinterpret_cast<const uint4*>(out + m * kYRow + (lane & 3) * 16);
                         if (p >= 0 && n < n_out) *reinterpret_cast<uint4*>(a.y + static_cast<size_t>(p) * n_out + n) = v4;
                     }
@@ -474,16 +542,17 @@ __global__ void __launch_bounds__(kLThreads, 1) experts_large_kernel(LargeArgs a
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.acc_empty[buf]);
+            if (lane == 0) mbar_arrive_leader(&bars.acc_empty[buf]);
             buf ^= 1;
             if (buf == 0) ph ^= 1;
         }
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync();  // neither CTA leaves, or frees tensor memory, before both are done
     if (warp == kMmaWarp) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc2(tmem, 512);
     }
 }
 
@@ -499,10 +568,10 @@ cudaError_t configure_experts_large() {
 
 cudaError_t launch_experts_large(const ExpertArgs& a, const DeviceInfo& d, cudaStream_t st) {
     const LargeArgs l{a, d.timeout_ns};
-    if (a.g == a.K) experts_large_kernel<0><<<d.num_sms, kLThreads, kSmemL, st>>>(l);
-    else if (a.g == 64) experts_large_kernel<2><<<d.num_sms, kLThreads, kSmemL, st>>>(l);
-    else if (a.g == 32) experts_large_kernel<4><<<d.num_sms, kLThreads, kSmemL, st>>>(l);
-    else experts_large_kernel<1><<<d.num_sms, kLThreads, kSmemL, st>>>(l);
+    if (a.g == a.K) experts_large_kernel<0><<<d.num_sms & ~1, kLThreads, kSmemL, st>>>(l);
+    else if (a.g == 64) experts_large_kernel<2><<<d.num_sms & ~1, kLThreads, kSmemL, st>>>(l);
+    else if (a.g == 32) experts_large_kernel<4><<<d.num_sms & ~1, kLThreads, kSmemL, st>>>(l);
+    else experts_large_kernel<1><<<d.num_sms & ~1, kLThreads, kSmemL, st>>>(l);
     return cudaGetLastError();
 }
 
