@@ -170,9 +170,10 @@ struct Walk {
     int CT, E, step_rt, step_ct;
     const int* start;
     const int* tiles;
+    const int* each;         // rows per tile of an expert
 
-    __device__ __forceinline__ Walk(int CT_, int E_, const int* s_start, const int* s_tiles)
-        : e(0), row0(0), nrows(0), CT(CT_), E(E_), start(s_start), tiles(s_tiles) {
+    __device__ __forceinline__ Walk(int CT_, int E_, const int* s_start, const int* s_tiles, const int* s_each)
+        : e(0), row0(0), nrows(0), CT(CT_), E(E_), start(s_start), tiles(s_tiles), each(s_each) {
         const unsigned grid = gridDim.x / 2, b = blockIdx.x / 2;
         step_rt = grid / CT;
         step_ct = grid % CT;
@@ -198,11 +199,9 @@ struct Walk {
             if (tiles[mid] <= rt_all) lo = mid; else hi = mid;
         }
         e = lo;
-        const int n = start[lo + 1] - start[lo], share = tiles[lo + 1] - tiles[lo];
-        const int each = ((n + share - 1) / share + 15) / 16 * 16;  // even shares, at most kRowsMax
-        const int first = (rt_all - tiles[lo]) * each;
+        const int first = (rt_all - tiles[lo]) * each[lo];
         row0 = start[lo] + first;
-        nrows = min(each, n - first);
+        nrows = min(each[lo], start[lo + 1] - row0);
     }
 };
 
@@ -211,7 +210,7 @@ template <int SL>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) experts_large_kernel(LargeArgs args) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ Bars bars;
-    __shared__ int s_start[kExMaxExperts + 1], s_tiles[kExMaxExperts + 1], s_scratch[kLThreads / 32];
+    __shared__ int s_start[kExMaxExperts + 1], s_tiles[kExMaxExperts + 1], s_each[kExMaxExperts], s_scratch[kLThreads / 32];
     __shared__ __align__(16) uint8_t stage_y[4 * kYBytes];
     __shared__ uint32_t s_tmem;
     __shared__ int s_stop;
@@ -235,6 +234,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
     }
     if (warp == kMmaWarp) tmem_alloc2(&s_tmem, 512);
     expert_table<kLThreads>(a.offsets, a.E, a.pairs, kRowsMax, s_start, s_tiles, s_scratch);
+    for (int e = tid; e < a.E; e += kLThreads) {
+        const int n = s_start[e + 1] - s_start[e], share = s_tiles[e + 1] - s_tiles[e];
+        s_each[e] = share ? ((n + share - 1) / share + 15) / 16 * 16 : 0;  // even shares, at most kRowsMax
+    }
     tc_fence_before();
     __syncthreads();
     cluster_sync();  // the barriers of both CTAs stand
@@ -243,7 +246,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
     const Ctl ctl{&s_stop, a.status, args.timeout_ns};
     const int KT = a.K / kTileK, chunks = a.K / kChunkK;
     const int CT = (a.N + 2 * kColsL - 1) / (2 * kColsL), NU = ex_units(a.N);
-    Walk t(CT, a.E, s_start, s_tiles);
+    Walk t(CT, a.E, s_start, s_tiles, s_each);
 
     if (warp < kGatherWarps) {
         // ---------------------------------------------------------------- rows of the activations
@@ -262,24 +265,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
             __syncwarp();
             if (lane == 0) mbar_arrive_leader(&bars.full[last]);
         };
-        int place[kQuads];  // the next tile's entries of the lists, read while this one is copied
+        // Entries of the lists of the next tile, read while this one is copied: lane l the rows l, l +
+        // 32, .. of this CTA's half; places behind its last row repeat that row.
+        int place[kHalfRows / 32];
         int have = 0;       // rows of that tile that this CTA holds
         auto read_rows = [&]() {
             const int half = t.done() ? 0 : (t.nrows + 15) / 16 * 8, first = rank * half;
-            have = t.done() ? 0 : min(half, t.nrows - first);
+            have = t.done() ? 0 : max(0, min(half, t.nrows - first));
 #pragma unroll
-            for (int j = 0; j < kQuads; ++j) place[j] = j * 4 + sub < have ? __ldg(a.rows + t.row0 + first + j * 4 + sub) : -1;
+            for (int j = 0; j < kHalfRows / 32; ++j)
+                place[j] = have > 0 ? __ldg(a.rows + t.row0 + first + min(j * 32 + lane, have - 1)) : 0;
         };
         read_rows();
         bool more = !t.done();
         while (ok && more) {
+            const int quads = (have + 3) / 4;
             int row[kQuads];
 #pragma unroll
-            for (int j = 0; j < kQuads; ++j) {
-                // rows behind the tile's last keep what was there: their sums are never stored
-                row[j] = -1;
-                if (static_cast<unsigned>(place[j]) < static_cast<unsigned>(a.pairs)) row[j] = row_of_pair(place[j], a);
-                else if (j * 4 + sub < have) atomicCAS(a.status, 0, 1 /* WQ_ERR_INVALID_ARG */);
+            for (int j = 0; j < kHalfRows / 32; ++j) {
+                // an entry that names no pair takes row 0: its sums are never stored
+                const bool good = static_cast<unsigned>(place[j]) < static_cast<unsigned>(a.pairs);
+                if (!good) atomicCAS(a.status, 0, 1 /* WQ_ERR_INVALID_ARG */);
+                const int mine = good ? row_of_pair(place[j], a) : 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) row[j * 8 + i] = __shfl_sync(kFull, mine, i * 4 + sub);
             }
             const unsigned tile_n = n;
             t.next();
@@ -294,7 +303,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
                 const uint8_t* src = reinterpret_cast<const uint8_t*>(a.a + c * kChunkK + piece * 8);
 #pragma unroll
                 for (int j = 0; j < kQuads; ++j)
-                    if (row[j] >= 0)
+                    if (j < quads)
                         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
                                          ((j & 1) ? dst_odd : dst_even) + stage * kBBytes + j * 512),
                                      "l"(src + static_cast<unsigned long long>(static_cast<unsigned>(row[j])) * row_bytes)
@@ -368,12 +377,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
         const int quarter = warp & 3, par = (warp - kDqWarp0) >> 2;
         const int gc = lane >> 2;
         constexpr int kS = SL ? SL : 1;
-        constexpr int kDepth = SL == 4 ? 2 : 3;  // k-blocks of codes in flight
+        constexpr int kDepth = 2;  // k-blocks of codes in flight
+        const int kb_per_group = SL == 1 ? a.g / kTileK : 1;
         uint4 w[kDepth][4];    // [(rt, h)]
         uint2 sc[kDepth][kS];  // scales of the columns (rt, h) as fp16
         uint32_t valid = 0, live = 0;  // bit d: slot d holds a k-block / one inside the weight
         int f_kb = par;
-        const uint8_t* f_codes = a.wp;
+        const uint8_t* f_at = a.wp;
         const uint8_t* f_scales = a.wp;
         bool f_live = false;
         auto open_tile = [&]() {  // step over the tiles until f_kb lies in one
@@ -385,7 +395,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
             const int u = (t.ct * 2 + rank) * 4 + quarter;
             f_live = u < NU;
             const uint8_t* we = a.wp + static_cast<size_t>(t.e) * a.expert_stride;
-            f_codes = we + static_cast<size_t>(u) * KT * kExUnitBytes + lane * 16;
+            f_at = we + (static_cast<size_t>(u) * KT + f_kb) * kExUnitBytes + lane * 16;
             f_scales = we + a.scale_offset + static_cast<size_t>(u) * (a.K / a.g) * (kExUnitN * 2) + gc * 8;
         };
         auto fetch = [&](int d) {
@@ -397,12 +407,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
             live = f_live ? live | (1u << d) : live & ~(1u << d);
             if (f_live) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    w[d][i] = ldg_stream16(f_codes + static_cast<size_t>(f_kb) * kExUnitBytes + i * 512);
+                for (int i = 0; i < 4; ++i) w[d][i] = ldg_stream16(f_at + i * 512);
+                f_at += 2 * kExUnitBytes;
                 if (SL) {
 #pragma unroll
                     for (int i = 0; i < kS; ++i) {
-                        const int grp = SL == 1 ? f_kb * kTileK / a.g : f_kb * SL + i;
+                        const int grp = SL == 1 ? (kb_per_group == 1 ? f_kb : f_kb / kb_per_group) : f_kb * SL + i;
                         sc[d][i] = __ldg(reinterpret_cast<const uint2*>(f_scales + static_cast<size_t>(grp) * (kExUnitN * 2)));
                     }
                 }
@@ -426,10 +436,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
 #pragma unroll
             for (int d = 0; d < kDepth; ++d) {
                 if (!ok || !((valid >> d) & 1u)) break;
+                uint32_t v[2][2][16];  // [half of the k-block][rt]
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const unsigned c = n + half;
-                    uint32_t v[2][16];
+                for (int half = 0; half < 2; ++half)
 #pragma unroll
                     for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
@@ -451,8 +460,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
                                     }
                                 }
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) v[rt][2 * (4 * b + i) + h] = p[i];
+                                for (int i = 0; i < 4; ++i) v[half][rt][2 * (4 * b + i) + h] = p[i];
                             }
+                const bool stored = (live >> d) & 1u;
+                fetch(d);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const unsigned c = n + half;
                     // the chunk four before has left the slot; the first four find it empty
                     if (c >= kSlotsA) {
                         const unsigned before = c - kSlotsA;
@@ -460,10 +474,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
                         if (!ok) break;
                         tc_fence_after();
                     }
-                    if ((live >> d) & 1u) {
+                    if (stored) {
                         const uint32_t slot = tbase + (c % kSlotsA) * (kChunkK / 2);
-                        tmem_st_16x128b_x8(slot, v[0]);
-                        tmem_st_16x128b_x8(slot + (16u << 16), v[1]);
+                        tmem_st_16x128b_x8(slot, v[half][0]);
+                        tmem_st_16x128b_x8(slot + (16u << 16), v[half][1]);
                         tmem_st_wait();
                         tc_fence_before();
                     }
@@ -471,7 +485,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
                     if (lane == 0) mbar_arrive_leader(&bars.full[c % kStagesB]);
                 }
                 n += 4;
-                if (ok) fetch(d);
             }
         }
     } else {
