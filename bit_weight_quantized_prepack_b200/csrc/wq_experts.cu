@@ -2,14 +2,14 @@
 // W = (q - 8) * s, fp32 sums, one rounding to fp16; gated: silu(gate) * up in the epilogue.
 // And the weighted sum of a token's pairs after the down product.
 //
-// experts_kernel (few rows per expert). Tile: 32 columns of one expert x up to 8*NB of its rows,
-// all of K. Eight warps take the tile's 128-row k-blocks in turn; a warp needs nothing from the
-// others until the sums are added, in the order of the warps, at the end. Every lane copies with
-// cp.async the codes and scales that it will itself multiply and its share of the activations (four
-// 16-byte chunks of codes, 4*NB of activations per k-block) into its warp's ring in shared memory,
-// so that the ring needs no barrier beyond the warp's. The weight is the 16-row operand of m16n8k16 (exact fp16
-// q - 8), the tokens are its 8 columns; each group's fp32 partial is scaled in fp32, so no weight
-// is rounded.
+// experts_kernel (few rows per expert). Tile: 32 columns of one expert x up to 8*NB of its rows, all
+// of K. A group of WK warps shares a tile, its 128-row k-blocks dealt in turn; the groups' tiles
+// follow one another without a break: a warp loads the codes of its next k-blocks, of this tile or
+// the next, into registers (16 bytes a lane, a whole fragment of the weight) and its activations
+// with cp.async into its own ring, and needs nothing from other warps until its group adds the
+// tile's sums, in the order of the warps, behind one barrier. The weight is the 16-row operand of
+// m16n8k16 (exact fp16 q - 8), the tokens are its 8 columns; each group's fp32 partial is scaled in
+// fp32, so no weight is rounded. Bound by HBM: a k-block of a tile is 2 KiB of codes.
 #include <cuda_runtime.h>
 #include <cuda_fp16.h>
 #include <cstdint>
@@ -22,14 +22,9 @@ namespace wq {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async8(void* dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+    // through L1: the warps of a CTA want the same rows at about the same time
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -57,181 +52,204 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// SL: scales per k-block and column (1, 2 or 4 groups of a k-block; 0: per-column, g == K)
-template <int NB, int SL>
-__global__ void __launch_bounds__(kThreads) experts_kernel(ExpertArgs a, int stages) {
-    extern __shared__ uint8_t smem_raw[];
-    constexpr int kStage = (4 + 4 * NB) * 512 + (SL ? SL : 1) * 256;
-    constexpr int kRows = 8 * NB;
-    __shared__ int s_start[kExMaxExperts + 1], s_tiles[kExMaxExperts + 1], s_scratch[kWarps];
+// NB: blocks of 8 rows. SL: scales per k-block and column (1, 2 or 4 groups of a k-block; 0:
+// per-column, g == K). W: warps. D: k-blocks in flight per warp.
+template <int NB_, int SL_>
+struct Small {
+    static constexpr int NB = NB_, SL = SL_;
+    static constexpr int W = NB == 4 ? 8 : 16;
+    static constexpr int D = NB == 1 && SL < 4 ? 3 : 2;
+    static constexpr int kRows = 8 * NB;
+    static constexpr int kRing = D * NB * 2048;            // bytes of a warp's ring
+    static constexpr int kRedRow = 36;                     // floats of a row of sums, with padding
+    static constexpr int kRed = kRows * kRedRow * 4;       // bytes of a warp's sums
+    static constexpr int kSmem = W * (kRing + kRed);
+};
+
+template <class C>
+__global__ void __launch_bounds__(C::W * 32, 1) experts_kernel(ExpertArgs a, int WK) {
+    constexpr int NB = C::NB, SL = C::SL, D = C::D, kS = SL ? SL : 1, kRows = C::kRows;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    __shared__ int s_start[kExMaxExperts + 1], s_tiles[kExMaxExperts + 1], s_each[kExMaxExperts], s_scratch[C::W];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int q = lane & 3, gc = lane >> 2;
-    uint8_t* ring = smem_raw + static_cast<size_t>(warp) * stages * kStage;
-    float* red = reinterpret_cast<float*>(smem_raw + static_cast<size_t>(kWarps) * stages * kStage);
-    expert_table<kThreads>(a.offsets, a.E, a.pairs, kRows, s_start, s_tiles, s_scratch);
+    const int group = warp / WK, ks = warp % WK, groups = C::W / WK;
+    uint8_t* ring = smem_raw + warp * C::kRing;
+    float* red = reinterpret_cast<float*>(smem_raw + C::W * C::kRing) + group * WK * (C::kRed / 4);
+    expert_table<C::W * 32>(a.offsets, a.E, a.pairs, kRows, s_start, s_tiles, s_scratch);
+    rows_per_tile<C::W * 32>(a.E, 8, s_start, s_tiles, s_each);
+    __syncthreads();
 
     const int KT = a.K / kTileK, NU = ex_units(a.N);
-    const long long tiles = static_cast<long long>(s_tiles[a.E]) * NU;
     const int n_out = a.gated ? a.N / 2 : a.N;
-    for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        // expert of the tile: the last e with s_tiles[e] * NU <= tile
-        const int rt_all = static_cast<int>(tile / NU);
-        int lo = 0, hi = a.E;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (s_tiles[mid] <= rt_all) lo = mid; else hi = mid;
-        }
-        const int e = lo;
-        const int ert = s_tiles[e + 1] - s_tiles[e];
-        const long long local = tile - static_cast<long long>(s_tiles[e]) * NU;
-        const int u = static_cast<int>(local / ert), rt = static_cast<int>(local % ert);
-        const int row0 = s_start[e] + rt * kRows;
-        const int nrows = min(kRows, s_start[e + 1] - row0);
-        const uint8_t* we = a.wp + static_cast<size_t>(e) * a.expert_stride;
-        const uint8_t* codes = we + static_cast<size_t>(u) * KT * kExUnitBytes + lane * 16;
-        const uint8_t* scales = we + a.scale_offset + static_cast<size_t>(u) * (a.K / a.g) * (kExUnitN * 2) + gc * 8;
-        const uint16_t* arow[NB];
+    const int kb_per_group = SL == 1 ? a.g / kTileK : 1;
+    Walk t(NU, a.E, blockIdx.x * groups + group, gridDim.x * groups, s_start, s_tiles, s_each);  // tile that is summed
+    Walk f = t;                                                                              // tile that is loaded
+
+    uint4 w[D][4];    // codes [(rt, h)]
+    uint2 sc[D][kS];  // scales of the columns (rt, h) as fp16
+    const uint8_t* f_codes = nullptr;
+    const uint8_t* f_scales = nullptr;
+    const uint16_t* arow[NB];
+    int f_kb = ks;
+    auto open_tile = [&]() {
+        if (f.done()) return;
+        const uint8_t* we = a.wp + static_cast<size_t>(f.e) * a.expert_stride;
+        f_codes = we + (static_cast<size_t>(f.ct) * KT + f_kb) * kExUnitBytes + lane * 16;
+        f_scales = we + a.scale_offset + static_cast<size_t>(f.ct) * (a.K / a.g) * (kExUnitN * 2) + gc * 8;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             const int r = b * 8 + gc;
             arow[b] = nullptr;
-            if (r < nrows) {
-                const int p = __ldg(a.rows + row0 + r);
+            if (r < f.nrows) {
+                const int p = __ldg(a.rows + f.row0 + r);
                 if (static_cast<unsigned>(p) < static_cast<unsigned>(a.pairs))
                     arow[b] = a.a + static_cast<size_t>(row_of_pair(p, a)) * a.K + q * 8;
                 else
                     atomicCAS(a.status, 0, 1 /* WQ_ERR_INVALID_ARG */);
             }
         }
-        auto issue = [&](int kb, int slot) {
-            if (kb < KT) {
-                uint8_t* st = ring + slot * kStage;
+    };
+    // load this warp's next k-block into slot d (compile-time): codes, scales, activations
+    auto fetch = [&](int d) {
+        if (!f.done()) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    cp_async16(st + i * 512 + lane * 16, codes + static_cast<size_t>(kb) * kExUnitBytes + i * 512);
+            for (int i = 0; i < 4; ++i) w[d][i] = ldg_stream16(f_codes + i * 512);
+            f_codes += WK * kExUnitBytes;
+            if (SL) {
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
-                    if (arow[b]) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            cp_async16(st + (4 + b * 4 + c) * 512 + q * 128 + gc * 16, arow[b] + kb * kTileK + c * 32);
-                    }
-                if (SL) {
-#pragma unroll
-                    for (int i = 0; i < SL; ++i) {
-                        const int grp = SL == 1 ? kb * kTileK / a.g : kb * SL + i;
-                        cp_async8(st + (4 + 4 * NB) * 512 + i * 256 + lane * 8, scales + static_cast<size_t>(grp) * (kExUnitN * 2));
-                    }
+                for (int i = 0; i < kS; ++i) {
+                    const int grp = SL == 1 ? (kb_per_group == 1 ? f_kb : f_kb / kb_per_group) : f_kb * SL + i;
+                    sc[d][i] = __ldg(reinterpret_cast<const uint2*>(f_scales + static_cast<size_t>(grp) * (kExUnitN * 2)));
                 }
             }
-            cp_async_commit();
-        };
-        float acc[2][NB][4];
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
 #pragma unroll
             for (int b = 0; b < NB; ++b)
+                if (arow[b]) {
+                    // rows behind the tile's last are not copied: what lies there meets no stored sum
+                    uint8_t* dst = ring + (d * NB + b) * 2048 + q * 128 + gc * 16;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[r][b][i] = 0.f;
-        int kb_issue = warp;
-        for (int s = 0; s < stages - 1; ++s, kb_issue += kWarps) issue(kb_issue, s);
-        int slot = 0;
-        for (int kb = warp; kb < KT; kb += kWarps) {
-            issue(kb_issue, slot == 0 ? stages - 1 : slot - 1);
-            kb_issue += kWarps;
-            // all groups but the newest stages - 1 have arrived
-            if (stages == 2) cp_async_wait<1>(); else if (stages == 3) cp_async_wait<2>(); else cp_async_wait<3>();
+                    for (int c = 0; c < 4; ++c) cp_async16(dst + c * 512, arow[b] + f_kb * kTileK + c * 32);
+                }
+            f_kb += WK;
+            if (f_kb >= KT) {
+                f_kb = ks;
+                f.next();
+                open_tile();
+            }
+        }
+        cp_async_commit();
+    };
+    open_tile();
+#pragma unroll
+    for (int d = 0; d < D; ++d) fetch(d);
+
+    float acc[2][NB][4];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[r][b][i] = 0.f;
+    int kb = ks, turn = 0;
+    while (!t.done()) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            if (t.done()) break;
+            cp_async_wait<D - 1>();
             __syncwarp();
-            const uint8_t* st = ring + slot * kStage;
-            uint4 w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4*>(st + i * 512 + lane * 16);
-            float d[2][NB][4];
+            const uint8_t* st = ring + d * NB * 2048 + lane * 16;
+            float s[2][NB][4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                if (SL && c % (4 / (SL ? SL : 1)) == 0) {
+                constexpr int kPer = SL ? 4 / kS : 4;  // 32-row blocks of a scale
+                if (SL && c % kPer == 0) {
 #pragma unroll
                     for (int r = 0; r < 2; ++r)
 #pragma unroll
                         for (int b = 0; b < NB; ++b)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) d[r][b][i] = 0.f;
+                            for (int i = 0; i < 4; ++i) s[r][b][i] = 0.f;
                 }
                 uint4 x[NB];
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    // rows behind the tile's last are not copied: what lies there meets no stored sum
-                    x[b] = ldmatrix4(st + (4 + b * 4 + c) * 512 + lane * 16);
-                }
+                for (int b = 0; b < NB; ++b)
+                    if (b == 0 || b * 8 < t.nrows) x[b] = ldmatrix4(st + b * 2048 + c * 512);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     uint32_t p0[4], p1[4];
-                    const uint4 w0 = w[2 * r], w1 = w[2 * r + 1];
+                    const uint4 w0 = w[d][2 * r], w1 = w[d][2 * r + 1];
                     dequant8(c == 0 ? w0.x : c == 1 ? w0.y : c == 2 ? w0.z : w0.w, p0);
                     dequant8(c == 0 ? w1.x : c == 1 ? w1.y : c == 2 ? w1.z : w1.w, p1);
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        float (&t)[4] = SL ? d[r][b] : acc[r][b];
-                        mma_16816(t, p0[0], p1[0], p0[1], p1[1], x[b].x, x[b].y);
-                        mma_16816(t, p0[2], p1[2], p0[3], p1[3], x[b].z, x[b].w);
-                    }
+                    for (int b = 0; b < NB; ++b)
+                        if (b == 0 || b * 8 < t.nrows) {
+                            float(&u)[4] = SL ? s[r][b] : acc[r][b];
+                            mma_16816(u, p0[0], p1[0], p0[1], p1[1], x[b].x, x[b].y);
+                            mma_16816(u, p0[2], p1[2], p0[3], p1[3], x[b].z, x[b].w);
+                        }
                 }
-                if (SL && c % (4 / (SL ? SL : 1)) == 4 / (SL ? SL : 1) - 1) {
-                    const uint2 sv = *reinterpret_cast<const uint2*>(st + (4 + 4 * NB) * 512 +
-                                                                     (c / (4 / (SL ? SL : 1))) * 256 + lane * 8);
+                if (SL && c % kPer == kPer - 1) {
+                    const uint2 sv = sc[d][c / kPer];
                     const float2 s0 = __half22float2(*reinterpret_cast<const __half2*>(&sv.x));
                     const float2 s1 = __half22float2(*reinterpret_cast<const __half2*>(&sv.y));
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        acc[0][b][0] += s0.x * d[0][b][0];
-                        acc[0][b][1] += s0.x * d[0][b][1];
-                        acc[0][b][2] += s0.y * d[0][b][2];
-                        acc[0][b][3] += s0.y * d[0][b][3];
-                        acc[1][b][0] += s1.x * d[1][b][0];
-                        acc[1][b][1] += s1.x * d[1][b][1];
-                        acc[1][b][2] += s1.y * d[1][b][2];
-                        acc[1][b][3] += s1.y * d[1][b][3];
-                    }
+                    for (int b = 0; b < NB; ++b)
+                        if (b == 0 || b * 8 < t.nrows) {
+                            acc[0][b][0] += s0.x * s[0][b][0];
+                            acc[0][b][1] += s0.x * s[0][b][1];
+                            acc[0][b][2] += s0.y * s[0][b][2];
+                            acc[0][b][3] += s0.y * s[0][b][3];
+                            acc[1][b][0] += s1.x * s[1][b][0];
+                            acc[1][b][1] += s1.x * s[1][b][1];
+                            acc[1][b][2] += s1.y * s[1][b][2];
+                            acc[1][b][3] += s1.y * s[1][b][3];
+                        }
                 }
             }
-            slot = slot + 1 == stages ? 0 : slot + 1;
-        }
-        cp_async_wait<0>();
-        // sums of the warps: red[warp][token][column]
-        float* mine = red + warp * (kRows * 33);
+            fetch(d);
+            kb += WK;
+            if (kb < KT) continue;
+
+            // the tile's end: sums of the group's warps, [warp][row][column]
+            float* mine = red + ks * (C::kRed / 4);
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+            for (int r = 0; r < 2; ++r)
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
+                for (int b = 0; b < NB; ++b)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    mine[(b * 8 + 2 * q + (i & 1)) * 33 + r * 16 + (i >> 1) * 8 + gc] = acc[r][b][i];
-        __syncthreads();
-        const int out_cols = a.gated ? 16 : 32;
-        for (int i = tid; i < nrows * out_cols; i += kThreads) {
-            const int m = i / out_cols, col = i % out_cols;
-            const int p = __ldg(a.rows + row0 + m);
-            const int v0 = a.gated ? (col >> 3) * 16 + (col & 7) : col;
-            float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) s0 += red[w * (kRows * 33) + m * 33 + v0];
-            if (a.gated) {
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) s1 += red[w * (kRows * 33) + m * 33 + v0 + 8];
+                    for (int i = 0; i < 4; ++i) {
+                        mine[(b * 8 + 2 * q + (i & 1)) * C::kRedRow + r * 16 + (i >> 1) * 8 + gc] = acc[r][b][i];
+                        acc[r][b][i] = 0.f;
+                    }
+            if (WK > 1) named_barrier_sync(1 + group, WK * 32); else __syncwarp();
+            const int out_cols = a.gated ? 16 : 32;
+            const uint8_t* we = a.wp + static_cast<size_t>(t.e) * a.expert_stride;
+            for (int i = ks * 32 + lane; i < t.nrows * out_cols; i += WK * 32) {
+                const int m = i / out_cols, col = i % out_cols;
+                const int p = __ldg(a.rows + t.row0 + m);
+                const int v0 = a.gated ? (col >> 3) * 16 + (col & 7) : col;
+                float s0 = 0.f, s1 = 0.f;
+                for (int k = 0; k < WK; ++k) s0 += red[k * (C::kRed / 4) + m * C::kRedRow + v0];
+                if (a.gated)
+                    for (int k = 0; k < WK; ++k) s1 += red[k * (C::kRed / 4) + m * C::kRedRow + v0 + 8];
+                if (!SL) {
+                    const __half* cs = reinterpret_cast<const __half*>(we + a.scale_offset) + static_cast<size_t>(t.ct) * kExUnitN;
+                    const int at = (v0 & 7) * 4 + (v0 >> 4) * 2 + ((v0 >> 3) & 1);
+                    s0 *= __half2float(cs[at]);
+                    if (a.gated) s1 *= __half2float(cs[at + 1]);
+                }
+                const float out = a.gated ? silu_mul(s0, s1) : s0;
+                const int n = t.ct * out_cols + col;
+                if (n < n_out && static_cast<unsigned>(p) < static_cast<unsigned>(a.pairs))
+                    a.y[static_cast<size_t>(p) * n_out + n] = __half_as_ushort(__float2half_rn(out));
             }
-            if (!SL) {
-                const __half* cs = reinterpret_cast<const __half*>(we + a.scale_offset) + static_cast<size_t>(u) * kExUnitN;
-                const int at = (v0 & 7) * 4 + (v0 >> 4) * 2 + ((v0 >> 3) & 1);
-                s0 *= __half2float(cs[at]);
-                if (a.gated) s1 *= __half2float(cs[at + 1]);
-            }
-            const float out = a.gated ? silu_mul(s0, s1) : s0;
-            const int n = u * out_cols + col;
-            if (n < n_out && static_cast<unsigned>(p) < static_cast<unsigned>(a.pairs))
-                a.y[static_cast<size_t>(p) * n_out + n] = __half_as_ushort(__float2half_rn(out));
+            if (WK > 1) named_barrier_sync(1 + group, WK * 32); else __syncwarp();
+            kb = ks;
+            t.next();
         }
-        __syncthreads();
     }
+    cp_async_wait<0>();
 }
 
 // Y[t] = sum over j of w[t, j] * yp[t * top_k + j], in the order of j, fp32; a choice outside
@@ -266,37 +284,49 @@ __global__ void __launch_bounds__(256) combine_kernel(const uint16_t* __restrict
 }
 
 template <int NB, int SL>
-struct Small {
-    static constexpr int kStage = (4 + 4 * NB) * 512 + (SL ? SL : 1) * 256;
-    static constexpr int kStages = NB == 1 ? 3 : 2;
-    static constexpr int kSmem = kWarps * kStages * kStage + kWarps * 8 * NB * 33 * 4;
-    static cudaError_t configure() {
-        return cudaFuncSetAttribute(experts_kernel<NB, SL>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+cudaError_t configure_small() {
+    using C = Small<NB, SL>;
+    return cudaFuncSetAttribute(experts_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+}
+
+template <int NB, int SL>
+cudaError_t launch_small(const ExpertArgs& a, int num_sms, cudaStream_t st) {
+    using C = Small<NB, SL>;
+    // Warps per tile: the count that gives the busiest warp the fewest k-blocks, a tile's end counted
+    // as one. The lists are on the device: taken to be spread over as many experts as there are pairs.
+    const long long experts = a.pairs < a.E ? a.pairs : a.E;
+    const long long per = (a.pairs + experts - 1) / experts;
+    const long long tiles = experts * ((per + C::kRows - 1) / C::kRows) * ex_units(a.N);
+    const int KT = a.K / kTileK;
+    int best = 1;
+    long long best_cost = -1;
+    for (int wk = 1; wk <= C::W && wk <= KT; wk *= 2) {
+        const long long workers = static_cast<long long>(num_sms) * (C::W / wk);
+        const long long cost = (tiles + workers - 1) / workers * ((KT + wk - 1) / wk + 1);
+        if (best_cost < 0 || cost < best_cost) {
+            best = wk;
+            best_cost = cost;
+        }
     }
-    static cudaError_t launch(const ExpertArgs& a, int num_sms, cudaStream_t st) {
-        // at most every pair a tile of its own; CTAs past the last tile return at once
-        const long long most = static_cast<long long>(a.pairs) * ex_units(a.N);
-        const int want = num_sms * (kSmem <= 110 * 1024 ? 2 : 1);
-        experts_kernel<NB, SL><<<static_cast<unsigned>(most < want ? most : want), kThreads, kSmem, st>>>(a, kStages);
-        return cudaGetLastError();
-    }
-};
+    experts_kernel<C><<<num_sms, C::W * 32, C::kSmem, st>>>(a, best);
+    return cudaGetLastError();
+}
 
 template <int NB>
 cudaError_t configure_nb() {
-    cudaError_t e = Small<NB, 0>::configure();
-    if (e == cudaSuccess) e = Small<NB, 1>::configure();
-    if (e == cudaSuccess) e = Small<NB, 2>::configure();
-    if (e == cudaSuccess) e = Small<NB, 4>::configure();
+    cudaError_t e = configure_small<NB, 0>();
+    if (e == cudaSuccess) e = configure_small<NB, 1>();
+    if (e == cudaSuccess) e = configure_small<NB, 2>();
+    if (e == cudaSuccess) e = configure_small<NB, 4>();
     return e;
 }
 
 template <int NB>
 cudaError_t launch_nb(const ExpertArgs& a, int num_sms, cudaStream_t st) {
-    if (a.g == a.K) return Small<NB, 0>::launch(a, num_sms, st);
-    if (a.g == 64) return Small<NB, 2>::launch(a, num_sms, st);
-    if (a.g == 32) return Small<NB, 4>::launch(a, num_sms, st);
-    return Small<NB, 1>::launch(a, num_sms, st);
+    if (a.g == a.K) return launch_small<NB, 0>(a, num_sms, st);
+    if (a.g == 64) return launch_small<NB, 2>(a, num_sms, st);
+    if (a.g == 32) return launch_small<NB, 4>(a, num_sms, st);
+    return launch_small<NB, 1>(a, num_sms, st);
 }
 
 }  // namespace
@@ -313,7 +343,7 @@ cudaError_t launch_experts(const ExpertArgs& a, const DeviceInfo& d, cudaStream_
     const long long per_expert = (static_cast<long long>(a.pairs) + a.E - 1) / a.E;
     const int num_sms = d.num_sms;
     if (per_expert > 16) return launch_experts_large(a, d, st);
-    if (per_expert <= 4) return launch_nb<1>(a, num_sms, st);
+    if (per_expert <= 2) return launch_nb<1>(a, num_sms, st);
     if (per_expert <= 8) return launch_nb<2>(a, num_sms, st);
     return launch_nb<4>(a, num_sms, st);
 }

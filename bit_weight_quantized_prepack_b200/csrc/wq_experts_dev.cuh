@@ -85,4 +85,65 @@ __device__ __forceinline__ int row_of_pair(int p, const ExpertArgs& a) {
 
 __device__ __forceinline__ float silu_mul(float gate, float up) { return __fdividef(gate, 1.0f + __expf(-gate)) * up; }
 
+// Rows of each of an expert's row tiles: even shares, rounded up to `unit` rows.
+template <int kBlock>
+__device__ void rows_per_tile(int E, int unit, const int* s_start, const int* s_tiles, int* s_each) {
+    for (int e = threadIdx.x; e < E; e += kBlock) {
+        const int n = s_start[e + 1] - s_start[e], share = s_tiles[e + 1] - s_tiles[e];
+        s_each[e] = share ? ((n + share - 1) / share + unit - 1) / unit * unit : 0;
+    }
+}
+
+// Walk of worker `first` of `workers` over the tiles: row tile rt_all of all experts' row tiles, column
+// tile ct of CT; the column tiles of one row tile are neighbours.
+struct Walk {
+    int rt_all, ct, e;       // position
+    int row0, nrows;         // rows of the tile: places row0 .. of the lists
+    int CT, E, step_rt, step_ct;
+    const int* start;
+    const int* tiles;
+    const int* each;
+
+    __device__ __forceinline__ Walk(int CT_, int E_, unsigned first, unsigned workers, const int* s_start,
+                                    const int* s_tiles, const int* s_each)
+        : e(0), row0(0), nrows(0), CT(CT_), E(E_), start(s_start), tiles(s_tiles), each(s_each) {
+        step_rt = workers / CT;
+        step_ct = workers % CT;
+        rt_all = first / CT;
+        ct = first % CT;
+        locate();
+    }
+    __device__ __forceinline__ bool done() const { return rt_all >= tiles[E]; }
+    __device__ __forceinline__ void next() {
+        rt_all += step_rt;
+        ct += step_ct;
+        if (ct >= CT) {
+            ct -= CT;
+            ++rt_all;
+        }
+        locate();
+    }
+    __device__ __forceinline__ void locate() {
+        if (done()) return;
+        int lo = e, hi = E;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (tiles[mid] <= rt_all) lo = mid; else hi = mid;
+        }
+        e = lo;
+        const int first = (rt_all - tiles[lo]) * each[lo];
+        row0 = start[lo] + first;
+        nrows = min(each[lo], start[lo + 1] - row0);
+    }
+};
+
+// 16 bytes that are read once: past L1.
+__device__ __forceinline__ uint4 ldg_stream16(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
 }  // namespace wq

@@ -154,57 +154,6 @@ __device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&v)[32]) {
         : "memory");
 }
 
-__device__ __forceinline__ uint4 ldg_stream16(const void* p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-
-// Walk of a CTA pair over the tiles: row tile rt_all of all experts' row tiles, column tile ct (256
-// columns); column tiles of one row tile are neighbours. Pair b takes tiles b, b + pairs, ...
-struct Walk {
-    int rt_all, ct, e;       // position
-    int row0, nrows;         // rows of the tile: places row0 .. of the lists
-    int CT, E, step_rt, step_ct;
-    const int* start;
-    const int* tiles;
-    const int* each;         // rows per tile of an expert
-
-    __device__ __forceinline__ Walk(int CT_, int E_, const int* s_start, const int* s_tiles, const int* s_each)
-        : e(0), row0(0), nrows(0), CT(CT_), E(E_), start(s_start), tiles(s_tiles), each(s_each) {
-        const unsigned grid = gridDim.x / 2, b = blockIdx.x / 2;
-        step_rt = grid / CT;
-        step_ct = grid % CT;
-        rt_all = b / CT;
-        ct = b % CT;
-        locate();
-    }
-    __device__ __forceinline__ bool done() const { return rt_all >= tiles[E]; }
-    __device__ __forceinline__ void next() {
-        rt_all += step_rt;
-        ct += step_ct;
-        if (ct >= CT) {
-            ct -= CT;
-            ++rt_all;
-        }
-        locate();
-    }
-    __device__ __forceinline__ void locate() {
-        if (done()) return;
-        int lo = e, hi = E;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (tiles[mid] <= rt_all) lo = mid; else hi = mid;
-        }
-        e = lo;
-        const int first = (rt_all - tiles[lo]) * each[lo];
-        row0 = start[lo] + first;
-        nrows = min(each[lo], start[lo + 1] - row0);
-    }
-};
-
 // SL as in the small kernel: scales per k-block and column; 0: per-column, applied in the epilogue.
 template <int SL>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) experts_large_kernel(LargeArgs args) {
@@ -234,10 +183,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
     }
     if (warp == kMmaWarp) tmem_alloc2(&s_tmem, 512);
     expert_table<kLThreads>(a.offsets, a.E, a.pairs, kRowsMax, s_start, s_tiles, s_scratch);
-    for (int e = tid; e < a.E; e += kLThreads) {
-        const int n = s_start[e + 1] - s_start[e], share = s_tiles[e + 1] - s_tiles[e];
-        s_each[e] = share ? ((n + share - 1) / share + 15) / 16 * 16 : 0;  // even shares, at most kRowsMax
-    }
+    rows_per_tile<kLThreads>(a.E, 16, s_start, s_tiles, s_each);
     tc_fence_before();
     __syncthreads();
     cluster_sync();  // the barriers of both CTAs stand
@@ -246,7 +192,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
     const Ctl ctl{&s_stop, a.status, args.timeout_ns};
     const int KT = a.K / kTileK, chunks = a.K / kChunkK;
     const int CT = (a.N + 2 * kColsL - 1) / (2 * kColsL), NU = ex_units(a.N);
-    Walk t(CT, a.E, s_start, s_tiles, s_each);
+    // column tiles of the same rows are neighbours; pair b takes tiles b, b + pairs, ...
+    Walk t(CT, a.E, blockIdx.x / 2, gridDim.x / 2, s_start, s_tiles, s_each);
 
     if (warp < kGatherWarps) {
         // ---------------------------------------------------------------- rows of the activations
