@@ -63,7 +63,9 @@ struct Small {
     static constexpr int kRing = D * NB * 2048;            // bytes of a warp's ring
     static constexpr int kRedRow = 36;                     // floats of a row of sums, with padding
     static constexpr int kRed = kRows * kRedRow * 4;       // bytes of a warp's sums
-    static constexpr int kSmem = W * (kRing + kRed);
+    // tiles that are open at a time: summed, D loaded, and the one after whose rows are known
+    static constexpr int kQueue = D + 2;
+    static constexpr int kSmem = W * (kRing + 2 * kRed);
 };
 
 template <class C>
@@ -83,36 +85,61 @@ __global__ void __launch_bounds__(C::W * 32, 1) experts_kernel(ExpertArgs a, int
     const int KT = a.K / kTileK, NU = ex_units(a.N);
     const int n_out = a.gated ? a.N / 2 : a.N;
     const int kb_per_group = SL == 1 ? a.g / kTileK : 1;
-    Walk t(NU, a.E, blockIdx.x * groups + group, gridDim.x * groups, s_start, s_tiles, s_each);  // tile that is summed
-    Walk f = t;                                                                              // tile that is loaded
+
+    // A warp's tiles between the loads that open them and the sums that end them.
+    struct Entry {
+        int e, ct, nrows;   // nrows 0: no tile left
+        int pair[kRows];    // -1: an entry of the lists that names no pair
+    };
+    __shared__ Entry s_queue[C::W][C::kQueue];
+    Walk next(NU, a.E, blockIdx.x * groups + group, gridDim.x * groups, s_start, s_tiles, s_each);  // to be opened
+    int place[NB];  // its rows' entries of the lists
+    auto read_rows = [&]() {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const int r = b * 8 + gc;
+            place[b] = !next.done() && r < next.nrows ? __ldg(a.rows + next.row0 + r) : -1;
+        }
+    };
+    read_rows();
 
     uint4 w[D][4];    // codes [(rt, h)]
     uint2 sc[D][kS];  // scales of the columns (rt, h) as fp16
     const uint8_t* f_codes = nullptr;
     const uint8_t* f_scales = nullptr;
     const uint16_t* arow[NB];
-    int f_kb = ks;
+    int f_kb = ks, f_at = 0;
+    bool f_valid = false;
     auto open_tile = [&]() {
-        if (f.done()) return;
-        const uint8_t* we = a.wp + static_cast<size_t>(f.e) * a.expert_stride;
-        f_codes = we + (static_cast<size_t>(f.ct) * KT + f_kb) * kExUnitBytes + lane * 16;
-        f_scales = we + a.scale_offset + static_cast<size_t>(f.ct) * (a.K / a.g) * (kExUnitN * 2) + gc * 8;
+        Entry& q_entry = s_queue[warp][f_at];
+        f_at = f_at + 1 == C::kQueue ? 0 : f_at + 1;
+        f_valid = !next.done();
+        if (!f_valid) {
+            if (lane == 0) q_entry.nrows = 0;
+            return;
+        }
+        const uint8_t* we = a.wp + static_cast<size_t>(next.e) * a.expert_stride;
+        f_codes = we + (static_cast<size_t>(next.ct) * KT + f_kb) * kExUnitBytes + lane * 16;
+        f_scales = we + a.scale_offset + static_cast<size_t>(next.ct) * (a.K / a.g) * (kExUnitN * 2) + gc * 8;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            const int r = b * 8 + gc;
-            arow[b] = nullptr;
-            if (r < f.nrows) {
-                const int p = __ldg(a.rows + f.row0 + r);
-                if (static_cast<unsigned>(p) < static_cast<unsigned>(a.pairs))
-                    arow[b] = a.a + static_cast<size_t>(row_of_pair(p, a)) * a.K + q * 8;
-                else
-                    atomicCAS(a.status, 0, 1 /* WQ_ERR_INVALID_ARG */);
-            }
+            const bool in = b * 8 + gc < next.nrows;
+            const bool good = static_cast<unsigned>(place[b]) < static_cast<unsigned>(a.pairs);
+            arow[b] = in && good ? a.a + static_cast<size_t>(row_of_pair(place[b], a)) * a.K + q * 8 : nullptr;
+            if (in && !good) atomicCAS(a.status, 0, 1 /* WQ_ERR_INVALID_ARG */);
+            if (q == 0) q_entry.pair[b * 8 + gc] = in && good ? place[b] : -1;
         }
+        if (lane == 0) {
+            q_entry.e = next.e;
+            q_entry.ct = next.ct;
+            q_entry.nrows = next.nrows;
+        }
+        next.next();
+        read_rows();
     };
     // load this warp's next k-block into slot d (compile-time): codes, scales, activations
     auto fetch = [&](int d) {
-        if (!f.done()) {
+        if (f_valid) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[d][i] = ldg_stream16(f_codes + i * 512);
             f_codes += WK * kExUnitBytes;
@@ -134,7 +161,6 @@ __global__ void __launch_bounds__(C::W * 32, 1) experts_kernel(ExpertArgs a, int
             f_kb += WK;
             if (f_kb >= KT) {
                 f_kb = ks;
-                f.next();
                 open_tile();
             }
         }
@@ -151,11 +177,26 @@ __global__ void __launch_bounds__(C::W * 32, 1) experts_kernel(ExpertArgs a, int
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[r][b][i] = 0.f;
-    int kb = ks, turn = 0;
-    while (!t.done()) {
+    int kb = ks, at = 0, turn = 0;
+    __syncwarp();
+    const Entry* t = &s_queue[warp][0];  // the tile that is summed
+    int nrows = t->nrows;
+    float cs0 = 1.f, cs1 = 1.f;  // column scales of this lane's output, g == K
+    auto column_scales = [&]() {
+        if (SL == 0 && nrows) {
+            const uint8_t* we = a.wp + static_cast<size_t>(t->e) * a.expert_stride;
+            const __half* cs = reinterpret_cast<const __half*>(we + a.scale_offset) + static_cast<size_t>(t->ct) * kExUnitN;
+            const int v0 = a.gated ? ((lane >> 3) & 1) * 16 + (lane & 7) : lane;
+            const int place = (v0 & 7) * 4 + (v0 >> 4) * 2 + ((v0 >> 3) & 1);
+            cs0 = __half2float(cs[place]);
+            if (a.gated) cs1 = __half2float(cs[place + 1]);
+        }
+    };
+    column_scales();
+    while (nrows) {
 #pragma unroll
         for (int d = 0; d < D; ++d) {
-            if (t.done()) break;
+            if (!nrows) break;
             cp_async_wait<D - 1>();
             __syncwarp();
             const uint8_t* st = ring + d * NB * 2048 + lane * 16;
@@ -174,7 +215,7 @@ __global__ void __launch_bounds__(C::W * 32, 1) experts_kernel(ExpertArgs a, int
                 uint4 x[NB];
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
-                    if (b == 0 || b * 8 < t.nrows) x[b] = ldmatrix4(st + b * 2048 + c * 512);
+                    if (b == 0 || b * 8 < nrows) x[b] = ldmatrix4(st + b * 2048 + c * 512);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     uint32_t p0[4], p1[4];
@@ -183,7 +224,7 @@ __global__ void __launch_bounds__(C::W * 32, 1) experts_kernel(ExpertArgs a, int
                     dequant8(c == 0 ? w1.x : c == 1 ? w1.y : c == 2 ? w1.z : w1.w, p1);
 #pragma unroll
                     for (int b = 0; b < NB; ++b)
-                        if (b == 0 || b * 8 < t.nrows) {
+                        if (b == 0 || b * 8 < nrows) {
                             float(&u)[4] = SL ? s[r][b] : acc[r][b];
                             mma_16816(u, p0[0], p1[0], p0[1], p1[1], x[b].x, x[b].y);
                             mma_16816(u, p0[2], p1[2], p0[3], p1[3], x[b].z, x[b].w);
@@ -195,7 +236,7 @@ __global__ void __launch_bounds__(C::W * 32, 1) experts_kernel(ExpertArgs a, int
                     const float2 s1 = __half22float2(*reinterpret_cast<const __half2*>(&sv.y));
 #pragma unroll
                     for (int b = 0; b < NB; ++b)
-                        if (b == 0 || b * 8 < t.nrows) {
+                        if (b == 0 || b * 8 < nrows) {
                             acc[0][b][0] += s0.x * s[0][b][0];
                             acc[0][b][1] += s0.x * s[0][b][1];
                             acc[0][b][2] += s0.y * s[0][b][2];
@@ -212,7 +253,9 @@ __global__ void __launch_bounds__(C::W * 32, 1) experts_kernel(ExpertArgs a, int
             if (kb < KT) continue;
 
             // the tile's end: sums of the group's warps, [warp][row][column]
-            float* mine = red + ks * (C::kRed / 4);
+            float* sums = red + turn * (C::W * C::kRed / 4);
+            turn ^= 1;
+            float* mine = sums + ks * (C::kRed / 4);
 #pragma unroll
             for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -222,31 +265,35 @@ __global__ void __launch_bounds__(C::W * 32, 1) experts_kernel(ExpertArgs a, int
                         mine[(b * 8 + 2 * q + (i & 1)) * C::kRedRow + r * 16 + (i >> 1) * 8 + gc] = acc[r][b][i];
                         acc[r][b][i] = 0.f;
                     }
+            // one barrier a tile: the sums of the next one go to the other buffer
             if (WK > 1) named_barrier_sync(1 + group, WK * 32); else __syncwarp();
-            const int out_cols = a.gated ? 16 : 32;
-            const uint8_t* we = a.wp + static_cast<size_t>(t.e) * a.expert_stride;
-            for (int i = ks * 32 + lane; i < t.nrows * out_cols; i += WK * 32) {
-                const int m = i / out_cols, col = i % out_cols;
-                const int p = __ldg(a.rows + t.row0 + m);
-                const int v0 = a.gated ? (col >> 3) * 16 + (col & 7) : col;
-                float s0 = 0.f, s1 = 0.f;
-                for (int k = 0; k < WK; ++k) s0 += red[k * (C::kRed / 4) + m * C::kRedRow + v0];
-                if (a.gated)
-                    for (int k = 0; k < WK; ++k) s1 += red[k * (C::kRed / 4) + m * C::kRedRow + v0 + 8];
-                if (!SL) {
-                    const __half* cs = reinterpret_cast<const __half*>(we + a.scale_offset) + static_cast<size_t>(t.ct) * kExUnitN;
-                    const int at = (v0 & 7) * 4 + (v0 >> 4) * 2 + ((v0 >> 3) & 1);
-                    s0 *= __half2float(cs[at]);
-                    if (a.gated) s1 *= __half2float(cs[at + 1]);
+            if (a.gated) {
+                const int col = lane & 15, v0 = (col >> 3) * 16 + (col & 7), n = t->ct * 16 + col;
+                for (int m = ks * 2 + (lane >> 4); m < nrows; m += WK * 2) {
+                    float gate = 0.f, up = 0.f;
+                    for (int k = 0; k < WK; ++k) {
+                        gate += sums[k * (C::kRed / 4) + m * C::kRedRow + v0];
+                        up += sums[k * (C::kRed / 4) + m * C::kRedRow + v0 + 8];
+                    }
+                    const int p = t->pair[m];
+                    const float out = silu_mul(gate * cs0, up * cs1);
+                    if (n < n_out && p >= 0) a.y[static_cast<size_t>(p) * n_out + n] = __half_as_ushort(__float2half_rn(out));
                 }
-                const float out = a.gated ? silu_mul(s0, s1) : s0;
-                const int n = t.ct * out_cols + col;
-                if (n < n_out && static_cast<unsigned>(p) < static_cast<unsigned>(a.pairs))
-                    a.y[static_cast<size_t>(p) * n_out + n] = __half_as_ushort(__float2half_rn(out));
+            } else {
+                const int n = t->ct * 32 + lane;
+                for (int m = ks; m < nrows; m += WK) {
+                    float out = 0.f;
+                    for (int k = 0; k < WK; ++k) out += sums[k * (C::kRed / 4) + m * C::kRedRow + lane];
+                    const int p = t->pair[m];
+                    if (n < n_out && p >= 0) a.y[static_cast<size_t>(p) * n_out + n] = __half_as_ushort(__float2half_rn(out * cs0));
+                }
             }
-            if (WK > 1) named_barrier_sync(1 + group, WK * 32); else __syncwarp();
             kb = ks;
-            t.next();
+            at = at + 1 == C::kQueue ? 0 : at + 1;
+            __syncwarp();
+            t = &s_queue[warp][at];
+            nrows = t->nrows;
+            column_scales();
         }
     }
     cp_async_wait<0>();
@@ -343,7 +390,7 @@ cudaError_t launch_experts(const ExpertArgs& a, const DeviceInfo& d, cudaStream_
     const long long per_expert = (static_cast<long long>(a.pairs) + a.E - 1) / a.E;
     const int num_sms = d.num_sms;
     if (per_expert > 16) return launch_experts_large(a, d, st);
-    if (per_expert <= 2) return launch_nb<1>(a, num_sms, st);
+    if (per_expert <= 4) return launch_nb<1>(a, num_sms, st);
     if (per_expert <= 8) return launch_nb<2>(a, num_sms, st);
     return launch_nb<4>(a, num_sms, st);
 }
