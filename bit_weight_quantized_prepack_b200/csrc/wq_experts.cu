@@ -383,6 +383,7 @@ cudaError_t configure_expert_kernels() {
     if (e == cudaSuccess) e = configure_nb<2>();
     if (e == cudaSuccess) e = configure_nb<4>();
     if (e == cudaSuccess) e = configure_experts_large();
+    if (e == cudaSuccess) e = configure_route();
     return e;
 }
 

@@ -81,7 +81,9 @@ struct ExpertArgs {
     int gated;
 };
 
-cudaError_t launch_route(const RouteArgs& a, cudaStream_t st);
+cudaError_t configure_route();
+// offsets and rows: null, or the lists of the choices too
+cudaError_t launch_route(const RouteArgs& a, int32_t* offsets, int32_t* rows, cudaStream_t st);
 cudaError_t launch_expert_lists(const int32_t* idx, int pairs, int E, int32_t* offsets, int32_t* rows,
                                 cudaStream_t st);
 cudaError_t launch_prepack_experts(const int32_t* Q, const uint16_t* s, int E, int K, int N, int g, int gated, void* Wp,

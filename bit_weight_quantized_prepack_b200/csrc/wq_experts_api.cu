@@ -105,11 +105,9 @@ int wq_route_experts(const void* logits, int logits_fp32, const float* bias, int
         a.group_top = group_top;
         a.renorm = renorm;
         a.scale = scale;
-        rc = status_of(launch_route(a, st));
-        if (rc) return rc;
+        return status_of(launch_route(a, offsets, rows, st));
     }
-    if (!offsets) return WQ_OK;
-    return status_of(launch_expert_lists(idx, T * top_k, E, offsets, rows, st));
+    return status_of(launch_expert_lists(idx, 0, E, offsets, rows, st));
 }
 
 int wq_expert_lists(const int32_t* idx, int T, int E, int top_k, int32_t* offsets, int32_t* rows, void* stream) {
