@@ -601,17 +601,22 @@ def wq_gemm_w4a8_fp16act(A: torch.Tensor, Wp: torch.Tensor, sw: torch.Tensor, N:
 
 
 # ------------------------------------------------------------------ experts
+# These calls are made per token of a decode step, where the host's microseconds count: a call costs
+# about 3 us of checks, 1.6 us per output tensor it allocates and 3-5 us in the library.
 _SCORES = {"softmax": 0, "sigmoid": 1}
 
 
 def _device_call(dev, stream, name, *args):
     """One library call on the tensors' device and, without a stream, on that device's current one."""
-    f = getattr(lib, name)
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(dev.index)  # current_stream(dev) without its 3 us
+    else:
+        handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
     if dev.index == torch.cuda.current_device():
-        _check(f(*args, _stream(stream)), name)
+        _check(getattr(lib, name)(*args, handle), name)
     else:
         with torch.cuda.device(dev):
-            _check(f(*args, _stream(stream)), name)
+            _check(getattr(lib, name)(*args, handle), name)
 
 
 def _scratch(nbytes, dev, stream):
@@ -625,6 +630,29 @@ def _scratch(nbytes, dev, stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=dev)
 
 
+def _want(t, dtype, name, shape):
+    """_tensor for an exact shape; the common case in one expression."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+        _tensor(t, dtype, name, shape=shape)
+
+
+def _one_device(first, *tensors, names):
+    """The CUDA device that all given tensors share (None among them is left out)."""
+    dev = first.device
+    if dev.type == "cuda":
+        for t in tensors:
+            if t is not None and t.device != dev:
+                break
+        else:
+            return dev
+    _on_one_cuda_device(**dict(zip(names, (first,) + tensors)))
+    return dev
+
+
+def _data(t):
+    return None if t is None else t.data_ptr()
+
+
 def wq_route_experts(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None = None, score: str = "softmax",
                      groups: int = 1, top_groups: int = 1, group_top: int = 1, renorm: bool = True,
                      scale: float = 1.0, lists: bool = False, idx: torch.Tensor | None = None,
@@ -636,30 +664,30 @@ def wq_route_experts(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None
     of ``groups`` runs of experts the ``top_groups`` with the largest sum of their ``group_top``
     best stay; the weights are divided by their sum (``renorm``) and multiplied by ``scale``."""
     T, E = _matrix(logits, "logits")
-    if logits.dtype not in (torch.float16, torch.float32):
-        raise TypeError(f"logits must be torch.float16 or torch.float32, got {logits.dtype}")
-    _tensor(logits, logits.dtype, "logits")
+    dtype = logits.dtype
+    if dtype is not torch.float16 and dtype is not torch.float32:
+        raise TypeError(f"logits must be torch.float16 or torch.float32, got {dtype}")
+    _want(logits, dtype, "logits", (T, E))
     if score not in _SCORES:
         raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
     if top_k <= 0:
         raise WqError(WQ_ERR_INVALID_ARG, "wq_route_experts")
     if bias is not None:
-        _tensor(bias, torch.float32, "bias", shape=(E,))
+        _want(bias, torch.float32, "bias", (E,))
     if idx is not None:
-        _tensor(idx, torch.int32, "idx", shape=(T, top_k))
+        _want(idx, torch.int32, "idx", (T, top_k))
     if w is not None:
-        _tensor(w, torch.float32, "w", shape=(T, top_k))
-    _on_one_cuda_device(logits=logits, bias=bias, idx=idx, w=w)
-    dev = logits.device
+        _want(w, torch.float32, "w", (T, top_k))
+    dev = _one_device(logits, bias, idx, w, names=("logits", "bias", "idx", "w"))
     if idx is None:
-        idx = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+        idx = torch.empty(T, top_k, dtype=torch.int32, device=dev)
     if w is None:
-        w = torch.empty((T, top_k), dtype=torch.float32, device=dev)
-    offsets = torch.empty((E + 1,), dtype=torch.int32, device=dev) if lists else None
-    rows = torch.empty((T * top_k,), dtype=torch.int32, device=dev) if lists else None
-    _device_call(dev, stream, "wq_route_experts", _ptr(logits), int(logits.dtype == torch.float32), _ptr(bias), T, E,
-                 top_k, _SCORES[score], groups, top_groups, group_top, int(bool(renorm)), scale, _ptr(idx), _ptr(w),
-                 _ptr(offsets), _ptr(rows))
+        w = torch.empty(T, top_k, dtype=torch.float32, device=dev)
+    offsets = torch.empty(E + 1, dtype=torch.int32, device=dev) if lists else None
+    rows = torch.empty(T * top_k, dtype=torch.int32, device=dev) if lists else None
+    _device_call(dev, stream, "wq_route_experts", logits.data_ptr(), int(dtype is torch.float32), _data(bias), T, E,
+                 top_k, _SCORES[score], groups, top_groups, group_top, int(bool(renorm)), scale, idx.data_ptr(),
+                 w.data_ptr(), _data(offsets), _data(rows))
     return (idx, w, offsets, rows) if lists else (idx, w)
 
 
@@ -668,17 +696,17 @@ def wq_expert_lists(idx: torch.Tensor, E: int, offsets: torch.Tensor | None = No
     """The pairs t * top_k + j by expert: idx int32 [T, top_k] -> offsets int32 [E + 1], rows int32
     [T * top_k]; pairs whose idx lies outside [0, E) are in no list."""
     T, top_k = _matrix(idx, "idx")
-    _tensor(idx, torch.int32, "idx")
+    _want(idx, torch.int32, "idx", (T, top_k))
     if offsets is not None:
-        _tensor(offsets, torch.int32, "offsets", shape=(E + 1,))
+        _want(offsets, torch.int32, "offsets", (E + 1,))
     if rows is not None:
-        _tensor(rows, torch.int32, "rows", shape=(T * top_k,))
-    _on_one_cuda_device(idx=idx, offsets=offsets, rows=rows)
+        _want(rows, torch.int32, "rows", (T * top_k,))
+    dev = _one_device(idx, offsets, rows, names=("idx", "offsets", "rows"))
     if offsets is None:
-        offsets = torch.empty((max(E, 0) + 1,), dtype=torch.int32, device=idx.device)
+        offsets = torch.empty(max(E, 0) + 1, dtype=torch.int32, device=dev)
     if rows is None:
-        rows = torch.empty((T * top_k,), dtype=torch.int32, device=idx.device)
-    _device_call(idx.device, stream, "wq_expert_lists", _ptr(idx), T, E, top_k, _ptr(offsets), _ptr(rows))
+        rows = torch.empty(T * top_k, dtype=torch.int32, device=dev)
+    _device_call(dev, stream, "wq_expert_lists", idx.data_ptr(), T, E, top_k, offsets.data_ptr(), rows.data_ptr())
     return offsets, rows
 
 
@@ -705,31 +733,34 @@ def wq_prepack_experts(Q: torch.Tensor, s: torch.Tensor, g: int, gated: bool = F
         raise ValueError("Q must be a 3-D tensor")
     E, K8, N = Q.shape
     K = K8 * 8
-    _tensor(Q, torch.int32, "Q")
+    _want(Q, torch.int32, "Q", (E, K8, N))
     nbytes = _experts_size(E, K, N, g, gated, "wq_prepack_experts")
-    _tensor(s, torch.float16, "s", shape=(E, K // g, N))
+    _want(s, torch.float16, "s", (E, K // g, N))
     if Wp is not None:
         _tensor(Wp, torch.uint8, "Wp", min_numel=nbytes)
-    _on_one_cuda_device(Q=Q, s=s, Wp=Wp)
+    dev = _one_device(Q, s, Wp, names=("Q", "s", "Wp"))
     if Wp is None:
-        Wp = torch.empty(nbytes, dtype=torch.uint8, device=Q.device)
-    _device_call(Q.device, stream, "wq_prepack_experts", _ptr(Q), _ptr(s), E, K, N, g, int(bool(gated)), _ptr(Wp))
+        Wp = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _device_call(dev, stream, "wq_prepack_experts", Q.data_ptr(), s.data_ptr(), E, K, N, g, int(bool(gated)),
+                 Wp.data_ptr())
     return Wp
 
 
 def wq_unpack_experts(Wp: torch.Tensor, E: int, K: int, N: int, g: int, gated: bool = False, stream=None):
     """Inverse of wq_prepack_experts: (Q int32 [E, K/8, N], s fp16 [E, K/g, N])."""
     _tensor(Wp, torch.uint8, "Wp", min_numel=_experts_size(E, K, N, g, gated, "wq_unpack_experts"))
-    _on_one_cuda_device(Wp=Wp)
-    Q = torch.empty((E, K // 8, N), dtype=torch.int32, device=Wp.device)
-    s = torch.empty((E, K // g, N), dtype=torch.float16, device=Wp.device)
-    _device_call(Wp.device, stream, "wq_unpack_experts", _ptr(Wp), E, K, N, g, int(bool(gated)), _ptr(Q), _ptr(s))
+    dev = _one_device(Wp, names=("Wp",))
+    Q = torch.empty(E, K // 8, N, dtype=torch.int32, device=dev)
+    s = torch.empty(E, K // g, N, dtype=torch.float16, device=dev)
+    _device_call(dev, stream, "wq_unpack_experts", Wp.data_ptr(), E, K, N, g, int(bool(gated)), Q.data_ptr(),
+                 s.data_ptr())
     return Q, s
 
 
-def _experts_args(A, Wp, offsets, rows, N, g, gated, where):
-    A_rows, K = _matrix(A, "A" if where == "wq_gemm_w4a16_experts" else "H")
-    _tensor(A, torch.float16, "A" if where == "wq_gemm_w4a16_experts" else "H")
+def _experts_args(A, Wp, offsets, rows, N, g, gated, name, where):
+    """Checks of what both products take; (rows of A, K, E)."""
+    A_rows, K = _matrix(A, name)
+    _want(A, torch.float16, name, (A_rows, K))
     _tensor(offsets, torch.int32, "offsets")
     _tensor(rows, torch.int32, "rows")
     if offsets.dim() != 1 or rows.dim() != 1:
@@ -744,21 +775,19 @@ def wq_gemm_w4a16_experts(A: torch.Tensor, Wp: torch.Tensor, offsets: torch.Tens
     """Every pair's token row times its expert's weight: A fp16 [T, K] -> Y fp16 [T * top_k, N], or
     [T * top_k, N / 2] = silu(gate) * up when ``gated`` (N counts both halves). offsets [E + 1] and
     rows [T * top_k] are the lists by expert; rows of Y of pairs in no list are left as they were."""
-    T, K, E = _experts_args(A, Wp, offsets, rows, N, g, gated, "wq_gemm_w4a16_experts")
+    T, K, E = _experts_args(A, Wp, offsets, rows, N, g, gated, "A", "wq_gemm_w4a16_experts")
     pairs = rows.numel()
-    if T == 0 or pairs % T:
-        if T or pairs:
-            raise ValueError(f"rows holds {pairs} pairs, not a multiple of A's {T} rows")
-    top_k = pairs // T if T else 1
-    shape = (pairs, N // 2 if gated else N)
+    if pairs % T if T else pairs:
+        raise ValueError(f"rows holds {pairs} pairs, not a multiple of A's {T} rows")
+    n_out = N // 2 if gated else N
     if Y is not None:
-        _tensor(Y, torch.float16, "Y", shape=shape)
-    _on_one_cuda_device(A=A, Wp=Wp, offsets=offsets, rows=rows, Y=Y)
+        _want(Y, torch.float16, "Y", (pairs, n_out))
+    dev = _one_device(A, Wp, offsets, rows, Y, names=("A", "Wp", "offsets", "rows", "Y"))
     if Y is None:
-        Y = torch.empty(shape, dtype=torch.float16, device=A.device)
+        Y = torch.empty(pairs, n_out, dtype=torch.float16, device=dev)
     if pairs:
-        _device_call(A.device, stream, "wq_gemm_w4a16_experts", _ptr(A), _ptr(Wp), _ptr(offsets), _ptr(rows), _ptr(Y),
-                     T, E, top_k, N, K, g, int(bool(gated)))
+        _device_call(dev, stream, "wq_gemm_w4a16_experts", A.data_ptr(), Wp.data_ptr(), offsets.data_ptr(),
+                     rows.data_ptr(), Y.data_ptr(), T, E, pairs // T, N, K, g, int(bool(gated)))
     return Y
 
 
@@ -772,27 +801,29 @@ def wq_gemm_w4a16_experts_combine(H: torch.Tensor, Wp: torch.Tensor, idx: torch.
     """Y fp16 [T, N] = sum over j of w[t, j] * (H[t * top_k + j] . W[idx[t, j]]); H fp16 [T * top_k, K]
     by pair, idx and w [T, top_k], the lists those of idx. Choices outside [0, E) add nothing."""
     T, top_k = _matrix(idx, "idx")
-    pairs, K, E = _experts_args(H, Wp, offsets, rows, N, g, False, "wq_gemm_w4a16_experts_combine")
-    _tensor(idx, torch.int32, "idx")
-    _tensor(w, torch.float32, "w", shape=(T, top_k))
+    pairs, K, E = _experts_args(H, Wp, offsets, rows, N, g, False, "H", "wq_gemm_w4a16_experts_combine")
+    _want(idx, torch.int32, "idx", (T, top_k))
+    _want(w, torch.float32, "w", (T, top_k))
     if top_k == 0:
         raise WqError(WQ_ERR_INVALID_ARG, "wq_gemm_w4a16_experts_combine")
     if pairs != T * top_k:
         raise ValueError(f"H must have {T * top_k} rows (one per pair), got {pairs}")
-    _tensor(rows, torch.int32, "rows", shape=(pairs,))
+    _want(rows, torch.int32, "rows", (pairs,))
     if Y is not None:
-        _tensor(Y, torch.float16, "Y", shape=(T, N))
+        _want(Y, torch.float16, "Y", (T, N))
     nbytes = wq_experts_scratch_bytes(T, top_k, N) if pairs else 0
     if scratch is not None:
         _tensor(scratch, torch.uint8, "scratch", min_numel=nbytes)
-    _on_one_cuda_device(H=H, Wp=Wp, idx=idx, w=w, offsets=offsets, rows=rows, Y=Y, scratch=scratch)
+    dev = _one_device(H, Wp, idx, w, offsets, rows, Y, scratch,
+                      names=("H", "Wp", "idx", "w", "offsets", "rows", "Y", "scratch"))
     if Y is None:
-        Y = torch.empty((T, N), dtype=torch.float16, device=H.device)
+        Y = torch.empty(T, N, dtype=torch.float16, device=dev)
     if pairs:
         if scratch is None:
-            scratch = _scratch(nbytes, H.device, stream)
-        _device_call(H.device, stream, "wq_gemm_w4a16_experts_combine", _ptr(H), _ptr(Wp), _ptr(idx), _ptr(w),
-                     _ptr(offsets), _ptr(rows), _ptr(Y), _ptr(scratch), scratch.numel(), T, E, top_k, N, K, g)
+            scratch = _scratch(nbytes, dev, stream)
+        _device_call(dev, stream, "wq_gemm_w4a16_experts_combine", H.data_ptr(), Wp.data_ptr(), idx.data_ptr(),
+                     w.data_ptr(), offsets.data_ptr(), rows.data_ptr(), Y.data_ptr(), scratch.data_ptr(),
+                     scratch.numel(), T, E, top_k, N, K, g)
     return Y
 
 
