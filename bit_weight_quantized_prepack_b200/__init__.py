@@ -91,7 +91,7 @@ def _load():
         "wq_prepack_experts": (I, [P, P, I, I, I, I, I, P, P]),
         "wq_unpack_experts": (I, [P, I, I, I, I, I, P, P, P]),
         "wq_gemm_w4a16_experts": (I, [P, P, P, P, P, I, I, I, I, I, I, I, P]),
-        "wq_experts_scratch_bytes": (Z, [I, I, I]),
+        "wq_experts_scratch_bytes": (Z, [I, I, I, I]),
         "wq_gemm_w4a16_experts_combine": (I, [P, P, P, P, P, P, P, P, Z, I, I, I, I, I, I, P]),
         "wq_workspace_bytes": (Z, [I, I, I, I]),
         "wq_workspace_reserve": (I, [Z, P]),
@@ -791,8 +791,8 @@ def wq_gemm_w4a16_experts(A: torch.Tensor, Wp: torch.Tensor, offsets: torch.Tens
     return Y
 
 
-def wq_experts_scratch_bytes(T: int, top_k: int, N: int) -> int:
-    return lib.wq_experts_scratch_bytes(T, top_k, N)
+def wq_experts_scratch_bytes(T: int, E: int, top_k: int, N: int) -> int:
+    return lib.wq_experts_scratch_bytes(T, E, top_k, N)
 
 
 def wq_gemm_w4a16_experts_combine(H: torch.Tensor, Wp: torch.Tensor, idx: torch.Tensor, w: torch.Tensor,
@@ -811,7 +811,7 @@ def wq_gemm_w4a16_experts_combine(H: torch.Tensor, Wp: torch.Tensor, idx: torch.
     _want(rows, torch.int32, "rows", (pairs,))
     if Y is not None:
         _want(Y, torch.float16, "Y", (T, N))
-    nbytes = wq_experts_scratch_bytes(T, top_k, N) if pairs else 0
+    nbytes = wq_experts_scratch_bytes(T, E, top_k, N) if pairs else 0
     if scratch is not None:
         _tensor(scratch, torch.uint8, "scratch", min_numel=nbytes)
     dev = _one_device(H, Wp, idx, w, offsets, rows, Y, scratch,
@@ -819,11 +819,11 @@ def wq_gemm_w4a16_experts_combine(H: torch.Tensor, Wp: torch.Tensor, idx: torch.
     if Y is None:
         Y = torch.empty(T, N, dtype=torch.float16, device=dev)
     if pairs:
-        if scratch is None:
+        if scratch is None and nbytes:
             scratch = _scratch(nbytes, dev, stream)
         _device_call(dev, stream, "wq_gemm_w4a16_experts_combine", H.data_ptr(), Wp.data_ptr(), idx.data_ptr(),
-                     w.data_ptr(), offsets.data_ptr(), rows.data_ptr(), Y.data_ptr(), scratch.data_ptr(),
-                     scratch.numel(), T, E, top_k, N, K, g)
+                     w.data_ptr(), offsets.data_ptr(), rows.data_ptr(), Y.data_ptr(), _data(scratch),
+                     0 if scratch is None else scratch.numel(), T, E, top_k, N, K, g)
     return Y
 
 

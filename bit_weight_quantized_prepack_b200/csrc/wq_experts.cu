@@ -299,6 +299,157 @@ __global__ void __launch_bounds__(C::W * 32, 1) experts_kernel(ExpertArgs a, int
     cp_async_wait<0>();
 }
 
+// The combined down product of a few tokens, without lists: a tile is 32 columns of one token's sum
+// over its experts, top_k * K long, whose 128-row k-blocks a group of WK warps takes in turn. A
+// weight's k-block is scaled by its group scale and the choice's weight together, in fp32. Experts
+// that two tokens share are read twice (the second time from L2), which is what limits this form to
+// few pairs; what it saves is a launch, the pairs' sums through memory and a rounding of each.
+template <int SL>
+__global__ void __launch_bounds__(512, 1) experts_token_kernel(ExpertArgs a, const int32_t* __restrict__ idx,
+                                                               const float* __restrict__ wt, int top_k, int WK) {
+    constexpr int W = 16, D = SL == 4 ? 2 : 3;
+    __shared__ __align__(16) uint8_t s_ring[W][D][256];  // the token's row of a k-block
+    __shared__ float s_sums[2][W][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int q = lane & 3, gc = lane >> 2;
+    const int group = warp / WK, ks = warp % WK, groups = W / WK;
+    const int KT = a.K / kTileK, NU = ex_units(a.N);
+    const int units = top_k * KT;
+    const int G = a.K / a.g;                                     // groups along K (1: per-column scales)
+    const int kb_per_group = SL == 1 && G > 1 ? a.g / kTileK : KT;
+    const unsigned tokens = a.pairs / top_k;
+    const unsigned step = gridDim.x * groups, step_t = step / NU, step_u = step % NU;
+
+    uint4 w[D][4];
+    uint2 sc[D][SL];
+    float wj[D];
+    unsigned good = 0;  // bit d: slot d holds a k-block of an expert
+    // the tile that is loaded; lane j has its j-th choice
+    unsigned f_t = (blockIdx.x * groups + group) / NU, f_u = (blockIdx.x * groups + group) % NU;
+    int f_unit = ks, my_e = -1;
+    float my_w = 0.f;
+    auto open_tile = [&]() {
+        if (f_t < tokens && lane < top_k) {
+            const size_t p = static_cast<size_t>(f_t) * top_k + lane;
+            my_e = __ldg(idx + p);
+            my_w = __ldg(wt + p);
+        }
+    };
+    auto fetch = [&](int d) {
+        if (f_t < tokens) {
+            const int j = f_unit / KT, kb = f_unit - j * KT;
+            const int e = __shfl_sync(kFull, my_e, j);
+            wj[d] = __shfl_sync(kFull, my_w, j);
+            good &= ~(1u << d);
+            if (static_cast<unsigned>(e) < static_cast<unsigned>(a.E)) {  // else the choice adds nothing
+                good |= 1u << d;
+                const uint8_t* we = a.wp + static_cast<size_t>(e) * a.expert_stride;
+                const uint8_t* codes = we + (static_cast<size_t>(f_u) * KT + kb) * kExUnitBytes + lane * 16;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[d][i] = ldg_stream16(codes + i * 512);
+#pragma unroll
+                for (int i = 0; i < SL; ++i) {
+                    const int grp = SL == 1 ? kb / kb_per_group : kb * SL + i;
+                    sc[d][i] = __ldg(reinterpret_cast<const uint2*>(
+                        we + a.scale_offset + (static_cast<size_t>(f_u) * G + grp) * (kExUnitN * 2) + gc * 8));
+                }
+                if (lane < 16)
+                    cp_async16(&s_ring[warp][d][lane * 16],
+                               a.a + (static_cast<size_t>(f_t) * top_k + j) * a.K + kb * kTileK + lane * 8);
+            }
+            f_unit += WK;
+            if (f_unit >= units) {
+                f_unit = ks;
+                f_t += step_t;
+                f_u += step_u;
+                if (f_u >= static_cast<unsigned>(NU)) {
+                    f_u -= NU;
+                    ++f_t;
+                }
+                open_tile();
+            }
+        }
+        cp_async_commit();
+    };
+    unsigned t = f_t, u = f_u;  // the tile that is summed
+    open_tile();
+#pragma unroll
+    for (int d = 0; d < D; ++d) fetch(d);
+    float acc[2][2] = {};  // columns (rt, h) of lane gc; every quad lane holds the same
+    int unit = ks, turn = 0;
+    while (t < tokens) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            if (t >= tokens) break;
+            cp_async_wait<D - 1>();
+            __syncwarp();
+            if ((good >> d) & 1u) {
+                // all eight rows of the activation operand are the token's
+                const uint8_t* st = &s_ring[warp][d][(lane >> 3) * 16];
+                float s[2][4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    constexpr int kPer = 4 / SL;
+                    if (c % kPer == 0) {
+#pragma unroll
+                        for (int r = 0; r < 2; ++r)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) s[r][i] = 0.f;
+                    }
+                    const uint4 x = ldmatrix4(st + c * 64);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        uint32_t p0[4], p1[4];
+                        const uint4 w0 = w[d][2 * r], w1 = w[d][2 * r + 1];
+                        dequant8(c == 0 ? w0.x : c == 1 ? w0.y : c == 2 ? w0.z : w0.w, p0);
+                        dequant8(c == 0 ? w1.x : c == 1 ? w1.y : c == 2 ? w1.z : w1.w, p1);
+                        mma_16816(s[r], p0[0], p1[0], p0[1], p1[1], x.x, x.y);
+                        mma_16816(s[r], p0[2], p1[2], p0[3], p1[3], x.z, x.w);
+                    }
+                    if (c % kPer == kPer - 1) {
+                        const uint2 sv = sc[d][c / kPer];
+                        const float2 s0 = __half22float2(*reinterpret_cast<const __half2*>(&sv.x));
+                        const float2 s1 = __half22float2(*reinterpret_cast<const __half2*>(&sv.y));
+                        acc[0][0] += s0.x * wj[d] * s[0][0];
+                        acc[0][1] += s0.y * wj[d] * s[0][2];
+                        acc[1][0] += s1.x * wj[d] * s[1][0];
+                        acc[1][1] += s1.y * wj[d] * s[1][2];
+                    }
+                }
+            }
+            fetch(d);
+            unit += WK;
+            if (unit < units) continue;
+            // the tile's end: the group's sums, in the order of its warps
+            float(*sums)[32] = s_sums[turn] + group * WK;
+            turn ^= 1;
+            if (q == 0) {
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) sums[ks][r * 16 + h * 8 + gc] = acc[r][h];
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) acc[r][0] = acc[r][1] = 0.f;
+            if (WK > 1) named_barrier_sync(1 + group, WK * 32); else __syncwarp();
+            if (ks == 0) {
+                float out = 0.f;
+                for (int k = 0; k < WK; ++k) out += sums[k][lane];
+                const int n = u * kExUnitN + lane;
+                if (n < a.N) a.y[static_cast<size_t>(t) * a.N + n] = __half_as_ushort(__float2half_rn(out));
+            }
+            unit = ks;
+            t += step_t;
+            u += step_u;
+            if (u >= static_cast<unsigned>(NU)) {
+                u -= NU;
+                ++t;
+            }
+        }
+    }
+    cp_async_wait<0>();
+}
+
 // Y[t] = sum over j of w[t, j] * yp[t * top_k + j], in the order of j, fp32; a choice outside
 // [0, E) adds nothing. One thread per 8 columns of a token.
 __global__ void __launch_bounds__(256) combine_kernel(const uint16_t* __restrict__ yp, const int32_t* __restrict__ idx,
@@ -336,25 +487,29 @@ cudaError_t configure_small() {
     return cudaFuncSetAttribute(experts_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
 }
 
-template <int NB, int SL>
-cudaError_t launch_small(const ExpertArgs& a, int num_sms, cudaStream_t st) {
-    using C = Small<NB, SL>;
-    // Warps per tile: the count that gives the busiest warp the fewest k-blocks, a tile's end counted
-    // as one. The lists are on the device: taken to be spread over as many experts as there are pairs.
-    const long long experts = a.pairs < a.E ? a.pairs : a.E;
-    const long long per = (a.pairs + experts - 1) / experts;
-    const long long tiles = experts * ((per + C::kRows - 1) / C::kRows) * ex_units(a.N);
-    const int KT = a.K / kTileK;
+// Warps per tile: the count that gives the busiest warp the fewest k-blocks, a tile's end counted as one.
+int warps_per_tile(long long tiles, int k_blocks, int warps, int num_sms) {
     int best = 1;
     long long best_cost = -1;
-    for (int wk = 1; wk <= C::W && wk <= KT; wk *= 2) {
-        const long long workers = static_cast<long long>(num_sms) * (C::W / wk);
-        const long long cost = (tiles + workers - 1) / workers * ((KT + wk - 1) / wk + 1);
+    for (int wk = 1; wk <= warps && wk <= k_blocks; wk *= 2) {
+        const long long workers = static_cast<long long>(num_sms) * (warps / wk);
+        const long long cost = (tiles + workers - 1) / workers * ((k_blocks + wk - 1) / wk + 1);
         if (best_cost < 0 || cost < best_cost) {
             best = wk;
             best_cost = cost;
         }
     }
+    return best;
+}
+
+template <int NB, int SL>
+cudaError_t launch_small(const ExpertArgs& a, int num_sms, cudaStream_t st) {
+    using C = Small<NB, SL>;
+    // the lists are on the device: taken to be spread over as many experts as there are pairs
+    const long long experts = a.pairs < a.E ? a.pairs : a.E;
+    const long long per = (a.pairs + experts - 1) / experts;
+    const long long tiles = experts * ((per + C::kRows - 1) / C::kRows) * ex_units(a.N);
+    const int best = warps_per_tile(tiles, a.K / kTileK, C::W, num_sms);
     experts_kernel<C><<<num_sms, C::W * 32, C::kSmem, st>>>(a, best);
     return cudaGetLastError();
 }
@@ -394,6 +549,20 @@ cudaError_t launch_experts(const ExpertArgs& a, const DeviceInfo& d, cudaStream_
     if (per_expert <= 4) return launch_nb<1>(a, num_sms, st);
     if (per_expert <= 8) return launch_nb<2>(a, num_sms, st);
     return launch_nb<4>(a, num_sms, st);
+}
+
+bool experts_token_form(int pairs, int E) { return pairs <= E / 4; }
+
+cudaError_t launch_experts_token(const ExpertArgs& a, const int32_t* idx, const float* w, int top_k, int num_sms,
+                                 cudaStream_t st) {
+    const long long tiles = static_cast<long long>(a.pairs / top_k) * ex_units(a.N);
+    const int wk = warps_per_tile(tiles, top_k * (a.K / kTileK), 16, num_sms);
+    const long long ctas = (tiles + 16 / wk - 1) / (16 / wk);
+    const unsigned grid = static_cast<unsigned>(ctas < num_sms ? ctas : num_sms);
+    if (a.g == 64) experts_token_kernel<2><<<grid, 512, 0, st>>>(a, idx, w, top_k, wk);
+    else if (a.g == 32) experts_token_kernel<4><<<grid, 512, 0, st>>>(a, idx, w, top_k, wk);
+    else experts_token_kernel<1><<<grid, 512, 0, st>>>(a, idx, w, top_k, wk);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_combine_experts(const uint16_t* yp, const int32_t* idx, const float* w, int T, int top_k, int E,

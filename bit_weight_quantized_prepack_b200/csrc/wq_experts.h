@@ -94,6 +94,11 @@ cudaError_t configure_expert_kernels();
 cudaError_t configure_experts_large();
 cudaError_t launch_experts(const ExpertArgs& a, const DeviceInfo& d, cudaStream_t st);
 cudaError_t launch_experts_large(const ExpertArgs& a, const DeviceInfo& d, cudaStream_t st);
+// Whether the combined product of so few pairs takes the form without lists and scratch.
+bool experts_token_form(int pairs, int E);
+// Y of args: [tokens, N]; a_div 1.
+cudaError_t launch_experts_token(const ExpertArgs& a, const int32_t* idx, const float* w, int top_k, int num_sms,
+                                 cudaStream_t st);
 cudaError_t launch_combine_experts(const uint16_t* yp, const int32_t* idx, const float* w, int T, int top_k, int E,
                                    int N, uint16_t* Y, cudaStream_t st);
 

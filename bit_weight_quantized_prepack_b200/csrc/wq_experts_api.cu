@@ -41,8 +41,8 @@ int check_lists(const int32_t* offsets, const int32_t* rows) {
     return WQ_OK;
 }
 
-int run_products(const uint16_t* A, const void* Wp, const int32_t* offsets, const int32_t* rows, uint16_t* Y, int T,
-                 int E, int top_k, int a_div, int N, int K, int g, int gated, cudaStream_t st, DeviceInfo* d) {
+ExpertArgs product_args(const uint16_t* A, const void* Wp, const int32_t* offsets, const int32_t* rows, uint16_t* Y,
+                        int T, int E, int top_k, int a_div, int N, int K, int g, int gated, const DeviceInfo& d) {
     ExpertArgs a;
     std::memset(&a, 0, sizeof(a));
     a.a = A;
@@ -50,7 +50,7 @@ int run_products(const uint16_t* A, const void* Wp, const int32_t* offsets, cons
     a.offsets = offsets;
     a.rows = rows;
     a.y = Y;
-    a.status = d->status;
+    a.status = d.status;
     a.expert_stride = ex_expert_stride(K, N, g);
     a.scale_offset = ex_scale_offset(K, N);
     a.pairs = T * top_k;
@@ -61,7 +61,7 @@ int run_products(const uint16_t* A, const void* Wp, const int32_t* offsets, cons
     a.K = K;
     a.g = g;
     a.gated = gated;
-    return status_of(launch_experts(a, *d, st));
+    return a;
 }
 
 }  // namespace
@@ -169,13 +169,11 @@ int wq_gemm_w4a16_experts(const uint16_t* A, const void* Wp, const int32_t* offs
     DeviceInfo d;
     rc = acquire_device(st, &d);
     if (rc) return rc;
-    return run_products(A, Wp, offsets, rows, Y, T, E, top_k, top_k, N, K, g, gated, st, &d);
+    return status_of(launch_experts(product_args(A, Wp, offsets, rows, Y, T, E, top_k, top_k, N, K, g, gated, d), d, st));
 }
 
-size_t wq_experts_scratch_bytes(int T, int top_k, int N) {
-    if (T < 0 || top_k <= 0 || N <= 0 || N % 8 || top_k > kExMaxTopK || T > kMaxTokens ||
-        static_cast<long long>(T) * top_k > kMaxPairs)
-        return 0;
+size_t wq_experts_scratch_bytes(int T, int E, int top_k, int N) {
+    if (check_counts(T, E, top_k) != WQ_OK || N <= 0 || N % 8 || experts_token_form(T * top_k, E)) return 0;
     return static_cast<size_t>(T) * top_k * N * 2;
 }
 
@@ -188,12 +186,13 @@ int wq_gemm_w4a16_experts_combine(const uint16_t* H, const void* Wp, const int32
     if (!Wp) return WQ_ERR_INVALID_ARG;
     if (!aligned(Wp, 16)) return WQ_ERR_MISALIGNED;
     if (T == 0) return WQ_OK;
-    if (!H || !Y || !idx || !w || !scratch) return WQ_ERR_INVALID_ARG;
+    const size_t need = wq_experts_scratch_bytes(T, E, top_k, N);
+    if (!H || !Y || !idx || !w || (need && !scratch)) return WQ_ERR_INVALID_ARG;
     rc = check_lists(offsets, rows);
     if (rc) return rc;
     if (!aligned(H, 16) || !aligned(Y, 16) || !aligned(scratch, 16) || !aligned(idx, 4) || !aligned(w, 4))
         return WQ_ERR_MISALIGNED;
-    if (scratch_bytes < wq_experts_scratch_bytes(T, top_k, N)) return WQ_ERR_INVALID_ARG;
+    if (scratch_bytes < need) return WQ_ERR_INVALID_ARG;
     // one thread of the summing kernel per 8 columns of a token
     if (static_cast<long long>(T) * (N / 8) >= (1ll << 31) * 128) return WQ_ERR_UNSUPPORTED_SHAPE;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -201,7 +200,10 @@ int wq_gemm_w4a16_experts_combine(const uint16_t* H, const void* Wp, const int32
     rc = acquire_device(st, &d);
     if (rc) return rc;
     uint16_t* yp = static_cast<uint16_t*>(scratch);
-    rc = run_products(H, Wp, offsets, rows, yp, T, E, top_k, 1, N, K, g, 0, st, &d);
+    if (experts_token_form(T * top_k, E))
+        return status_of(launch_experts_token(product_args(H, Wp, offsets, rows, Y, T, E, top_k, 1, N, K, g, 0, d), idx, w,
+                                              top_k, d.num_sms, st));
+    rc = status_of(launch_experts(product_args(H, Wp, offsets, rows, yp, T, E, top_k, 1, N, K, g, 0, d), d, st));
     if (rc) return rc;
     return status_of(launch_combine_experts(yp, idx, w, T, top_k, E, N, Y, st));
 }

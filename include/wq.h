@@ -326,8 +326,10 @@ WQ_API int wq_gemm_w4a16_noalloc(const uint16_t* A, const void* Wp, uint16_t* Y,
  * wq_gemm_w4a16_experts_combine: Y[t, n] = sum over j of w[t, j] * (H[t * top_k + j] . W_e[:, n]),
  * e = idx[t, j]; choices outside [0, E) add nothing (a token without any gets zeros). H fp16
  * [T * top_k, K] by pair, Y fp16 [T, N], and idx, w and the lists as wq_route_experts gives them
- * (the lists are those of idx). The sum runs over j in order, in fp32. scratch:
- * wq_experts_scratch_bytes(T, top_k, N) bytes that the call may write until it has completed. */
+ * (the lists are those of idx). The sum is fp32: of each pair's product rounded to fp16, over j in
+ * order, or for few pairs (T * top_k <= E / 4) of the unrounded products. scratch:
+ * wq_experts_scratch_bytes(T, E, top_k, N) bytes that the call may write until it has completed (0
+ * for few pairs: it may then be null). */
 WQ_API int wq_route_experts(const void* logits, int logits_fp32, const float* bias, int T, int E, int top_k, int score,
                  int groups, int top_groups, int group_top, int renorm, float scale, int32_t* idx, float* w,
                  int32_t* offsets, int32_t* rows, void* stream);
@@ -339,7 +341,7 @@ WQ_API int wq_unpack_experts(const void* Wp, int E, int K, int N, int g, int gat
                  void* stream);
 WQ_API int wq_gemm_w4a16_experts(const uint16_t* A, const void* Wp, const int32_t* offsets, const int32_t* rows,
                  uint16_t* Y, int T, int E, int top_k, int N, int K, int g, int gated, void* stream);
-WQ_API size_t wq_experts_scratch_bytes(int T, int top_k, int N);
+WQ_API size_t wq_experts_scratch_bytes(int T, int E, int top_k, int N);
 WQ_API int wq_gemm_w4a16_experts_combine(const uint16_t* H, const void* Wp, const int32_t* idx, const float* w,
                  const int32_t* offsets, const int32_t* rows, uint16_t* Y, void* scratch, size_t scratch_bytes,
                  int T, int E, int top_k, int N, int K, int g, void* stream);

@@ -151,11 +151,12 @@ def test_host_side_argument_checks():
 
     def comb(H=ok, idx=ok, w=ok, Y=ok, scratch=ok, nbytes=1 << 20, T=4, E=8, k=2, N=32, K=128, g=128):
         return L.wq_gemm_w4a16_experts_combine(H, ok, idx, w, ok, ok, Y, scratch, nbytes, T, E, k, N, K, g, None)
-    need = wq.wq_experts_scratch_bytes(4, 2, 32)
+    need = wq.wq_experts_scratch_bytes(4, 8, 2, 32)
     assert need > 0 and comb(nbytes=need - 1) == INV and comb(scratch=None) == INV and comb(scratch=P(0x10004)) == MIS
     assert comb(idx=None) == INV and comb(w=None) == INV and comb(H=None) == INV and comb(w=odd) == MIS
     assert comb(T=0, H=None, idx=None, w=None, Y=None, scratch=None) == wq.WQ_OK
-    assert wq.wq_experts_scratch_bytes(-1, 2, 32) == 0 and wq.wq_experts_scratch_bytes(4, 33, 32) == 0
+    assert wq.wq_experts_scratch_bytes(-1, 8, 2, 32) == 0 and wq.wq_experts_scratch_bytes(4, 64, 33, 32) == 0
+    assert wq.wq_experts_scratch_bytes(4, 32, 2, 32) == 0  # few pairs: the form without scratch
 
 
 # ------------------------------------------------------------------ the binding refuses before any call
@@ -217,7 +218,7 @@ def test_products_refuse(rec, over, err):
     ({"idx": torch.zeros((3, 2), dtype=torch.int64)}, TypeError),
     ({"rows": torch.zeros(7, dtype=torch.int32)}, ValueError),
     ({"Y": torch.zeros((6, 48), dtype=torch.float16)}, ValueError),
-    ({"scratch": torch.zeros(8, dtype=torch.uint8)}, ValueError),
+    ({"scratch": torch.zeros(8, dtype=torch.uint8)}, ValueError), ({"scratch": torch.zeros(999)}, TypeError),
     ({"idx": torch.zeros((3, 0), dtype=torch.int32)}, wq.WqError),
     ({}, TypeError),
 ])

@@ -187,6 +187,13 @@ PRODUCTS = [
     (130, 128, 16, 128, 1100, 4, 1, 0),
     (1024, 128, 16, 128, 50, 32, 0, 0),
     (3, 256, 528, 64, 1025, 3, 0, 0),
+    # few pairs of many experts
+    (64, 768, 264, 128, 1, 8, 0, 0),
+    (33, 384, 48, 32, 2, 4, 0, 0),
+    (128, 256, 144, 64, 3, 8, 0, 0.4),
+    (16, 512, 80, 512, 4, 1, 0, 0),
+    (40, 1280, 72, 640, 5, 2, 0, 0.4),
+    (1024, 128, 8, 128, 200, 1, 0, 0.1),
 ]
 
 
@@ -221,11 +228,12 @@ def test_combine(E, K, N, g, T, k, skew, padded):
     Wp = wq.wq_prepack_experts(dev(d["Q"]), dev(d["s"]), g)
     args = (dev(d["A"]), Wp, dev(d["idx"]), dev(d["w"]), dev(d["offsets"]), dev(d["rows"]), N, g)
     # a scratch of NaN: nothing of what it held may enter
-    scratch = torch.full((wq.wq_experts_scratch_bytes(T, k, N),), 255, dtype=torch.uint8, device="cuda")
+    scratch = torch.full((wq.wq_experts_scratch_bytes(T, E, k, N),), 255, dtype=torch.uint8, device="cuda")
     Y = wq.wq_gemm_w4a16_experts_combine(*args, scratch=scratch)
     status_ok()
     y, ad = oracle.experts_product(d["A"], d["Q"], d["s"], g, d["idx"], by_pair=True)
     ref = oracle.experts_combine(y, d["idx"], d["w"])
+    # a bound for pairs that are rounded before the sum also holds where they are not
     bound = combine_bound(y, ad, d["idx"], d["w"], K, g < K and large_rows(T, k, E))
     err = np.abs(f64(Y) - ref)
     assert np.all(err <= bound), (err / bound).max()
