@@ -414,11 +414,14 @@ int noalloc_device(int* dev_out, NoAllocDevice** out) {
 namespace wq {
 
 int acquire_device(cudaStream_t stream, DeviceInfo* info) {
-    std::lock_guard<std::mutex> lock(g_mu);
     int dev = 0;
-    DeviceState* d = nullptr;
-    const int rc = require_device(&dev, &d, stream, true);
-    if (rc) return rc;
+    if (cudaGetDevice(&dev) != cudaSuccess) return WQ_ERR_CUDA;
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceState* d = &g_devices[dev];
+    if (!d->init || !d->supported) {  // first call on the device, or one that is refused
+        const int rc = require_device(&dev, &d, stream, true);
+        if (rc) return rc;
+    }
     info->num_sms = d->num_sms;
     info->status = d->status;
     info->encode = reinterpret_cast<void*>(g_encode);

@@ -3,13 +3,15 @@
 // And the weighted sum of a token's pairs after the down product.
 //
 // experts_kernel (few rows per expert). Tile: 32 columns of one expert x up to 8*NB of its rows, all
-// of K. A group of WK warps shares a tile, its 128-row k-blocks dealt in turn; the groups' tiles
-// follow one another without a break: a warp loads the codes of its next k-blocks, of this tile or
-// the next, into registers (16 bytes a lane, a whole fragment of the weight) and its activations
-// with cp.async into its own ring, and needs nothing from other warps until its group adds the
-// tile's sums, in the order of the warps, behind one barrier. The weight is the 16-row operand of
-// m16n8k16 (exact fp16 q - 8), the tokens are its 8 columns; each group's fp32 partial is scaled in
-// fp32, so no weight is rounded. Bound by HBM: a k-block of a tile is 2 KiB of codes.
+// of K. A CTA has an equal run of all tiles, as segments of one row tile each, whose rows it keeps
+// in shared memory. Each of its 16 warps has an equal run of a segment's k-blocks (tile after tile,
+// 2 KiB of codes each, contiguous in memory) and streams them, across segments, into registers: 16
+// bytes a lane, a whole fragment of the weight. The weight is the 16-row operand of m16n8k16 (exact
+// fp16 q - 8), the tokens are its 8 columns; each scale multiplies its fp32 partial, so no weight is
+// rounded. A tile whose k-blocks lie with several warps is summed by the one that has the first, in
+// the order of the warps. Bound by HBM in the limit; the rows stay in shared memory because every SM
+// wants the same few at the same time: through a ring per warp, past L1, up_wide took 148 us, with L1
+// 85.
 #include <cuda_runtime.h>
 #include <cuda_fp16.h>
 #include <cstdint>
@@ -53,122 +55,174 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
 }
 
 // NB: blocks of 8 rows. SL: scales per k-block and column (1, 2 or 4 groups of a k-block; 0:
-// per-column, g == K). W: warps. D: k-blocks in flight per warp.
-template <int NB_, int SL_>
+// per-column, g == K). W: warps. With one k-block ahead of the one in hand, 24 warps of 80 registers
+// hide more than 16 of 128 with three (up_wide 72.6 us against 84.4; 28 warps 74.6, 32 76.5).
+template <int NB_, int SL_, int W_>
 struct Small {
-    static constexpr int NB = NB_, SL = SL_;
-    static constexpr int W = NB == 4 ? 8 : 16;
-    static constexpr int D = NB == 1 && SL < 4 ? 3 : 2;
+    static constexpr int NB = NB_, SL = SL_, W = W_;
     static constexpr int kRows = 8 * NB;
-    static constexpr int kRing = D * NB * 2048;            // bytes of a warp's ring
-    static constexpr int kRedRow = 36;                     // floats of a row of sums, with padding
-    static constexpr int kRed = kRows * kRedRow * 4;       // bytes of a warp's sums
-    // tiles that are open at a time: summed, D loaded, and the one after whose rows are known
-    static constexpr int kQueue = D + 2;
-    static constexpr int kSmem = W * (kRing + 2 * kRed);
+    static constexpr int kSumRow = 36;                     // floats of a row of sums, with padding
+    static constexpr int kSums = kRows * kSumRow;          // floats of a tile's sums
+    static constexpr size_t rows_bytes(int K) { return static_cast<size_t>(kRows) * K * 2; }
+    static constexpr size_t kFixed = static_cast<size_t>(W) * 2 * kSums * 4;
+    // shared memory with one or two places for the rows, and whether it fits
+    static constexpr size_t kMost = 232448 - 16384;        // less than the tables' static part
+    static size_t smem(int K, int places) { return kFixed + places * rows_bytes(K); }
+    static int places(int K) { return smem(K, 2) <= kMost ? 2 : smem(K, 1) <= kMost ? 1 : 0; }
 };
 
 template <class C>
-__global__ void __launch_bounds__(C::W * 32, 1) experts_kernel(ExpertArgs a, int WK) {
-    constexpr int NB = C::NB, SL = C::SL, D = C::D, kS = SL ? SL : 1, kRows = C::kRows;
+__global__ void __launch_bounds__(C::W * 32, 1) experts_kernel(ExpertArgs a, int places) {
+    constexpr int NB = C::NB, SL = C::SL, W = C::W, kS = SL ? SL : 1, kRows = C::kRows;
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    __shared__ int s_start[kExMaxExperts + 1], s_tiles[kExMaxExperts + 1], s_each[kExMaxExperts], s_scratch[C::W];
+    __shared__ int s_start[kExMaxExperts + 1], s_tiles[kExMaxExperts + 1], s_each[kExMaxExperts], s_scratch[W];
+    __shared__ int s_pair[2][kRows];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int q = lane & 3, gc = lane >> 2;
-    const int group = warp / WK, ks = warp % WK, groups = C::W / WK;
-    uint8_t* ring = smem_raw + warp * C::kRing;
-    float* red = reinterpret_cast<float*>(smem_raw + C::W * C::kRing) + group * WK * (C::kRed / 4);
-    expert_table<C::W * 32>(a.offsets, a.E, a.pairs, kRows, s_start, s_tiles, s_scratch);
-    rows_per_tile<C::W * 32>(a.E, 8, s_start, s_tiles, s_each);
+    float* sums = reinterpret_cast<float*>(smem_raw);          // [W][2][kSums]
+    uint8_t* s_rows = smem_raw + C::kFixed;
+    const size_t rows_bytes = C::rows_bytes(a.K);
+    expert_table<W * 32>(a.offsets, a.E, a.pairs, kRows, s_start, s_tiles, s_scratch);
+    rows_per_tile<W * 32>(a.E, 8, s_start, s_tiles, s_each);
     __syncthreads();
 
-    const int KT = a.K / kTileK, NU = ex_units(a.N);
+    const int KT = a.K / kTileK, NU = ex_units(a.N), G = a.K / a.g;
     const int n_out = a.gated ? a.N / 2 : a.N;
     const int kb_per_group = SL == 1 ? a.g / kTileK : 1;
+    const long long tiles = static_cast<long long>(s_tiles[a.E]) * NU;
+    const long long tile0 = tiles * blockIdx.x / gridDim.x, tile1 = tiles * (blockIdx.x + 1ll) / gridDim.x;
 
-    // A warp's tiles between the loads that open them and the sums that end them.
-    struct Entry {
-        int e, ct, nrows;   // nrows 0: no tile left
-        int pair[kRows];    // -1: an entry of the lists that names no pair
+    // A segment: the column tiles u0 .. u1 - 1 of one row tile; the CTA's tiles are a run of segments.
+    struct Segment {
+        int e, rt, u0, u1, row0, nrows;  // nrows 0: none left
     };
-    __shared__ Entry s_queue[C::W][C::kQueue];
-    Walk next(NU, a.E, blockIdx.x * groups + group, gridDim.x * groups, s_start, s_tiles, s_each);  // to be opened
-    int place[NB];  // its rows' entries of the lists
-    auto read_rows = [&]() {
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            const int r = b * 8 + gc;
-            place[b] = !next.done() && r < next.nrows ? __ldg(a.rows + next.row0 + r) : -1;
+    auto segment_at = [&](long long tile, int e) {
+        Segment s{e, 0, 0, 0, 0, 0};
+        if (tile >= tile1) return s;
+        s.rt = static_cast<int>(tile / NU);
+        s.u0 = static_cast<int>(tile - static_cast<long long>(s.rt) * NU);
+        s.u1 = static_cast<int>(min(static_cast<long long>(NU), s.u0 + (tile1 - tile)));
+        int lo = e, hi = a.E;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s_tiles[mid] <= s.rt) lo = mid; else hi = mid;
         }
+        s.e = lo;
+        const int first = (s.rt - s_tiles[lo]) * s_each[lo];
+        s.row0 = s_start[lo] + first;
+        s.nrows = min(s_each[lo], s_start[lo + 1] - s.row0);
+        return s;
     };
-    read_rows();
+    auto after = [&](const Segment& s) { return segment_at(static_cast<long long>(s.rt) * NU + s.u1, s.e); };
+    // this warp's run of a segment's k-blocks, the segment's tiles one after another
+    auto run_of = [&](const Segment& s, int w, int* beg, int* end) {
+        const int units = (s.u1 - s.u0) * KT, per = (units + W - 1) / W;
+        *beg = min(w * per, units);
+        *end = min((w + 1) * per, units);
+    };
 
-    uint4 w[D][4];    // codes [(rt, h)]
-    uint2 sc[D][kS];  // scales of the columns (rt, h) as fp16
+    // ---- loads of the weights, across segments
+    uint4 w[4];    // codes [(rt, h)] of the next k-block
+    uint2 sc[kS];  // scales of the columns (rt, h) as fp16
+    Segment f = segment_at(tile0, 0);
+    int f_left = 0, f_kb = 0;
     const uint8_t* f_codes = nullptr;
     const uint8_t* f_scales = nullptr;
-    const uint16_t* arow[NB];
-    int f_kb = ks, f_at = 0;
-    bool f_valid = false;
-    auto open_tile = [&]() {
-        Entry& q_entry = s_queue[warp][f_at];
-        f_at = f_at + 1 == C::kQueue ? 0 : f_at + 1;
-        f_valid = !next.done();
-        if (!f_valid) {
-            if (lane == 0) q_entry.nrows = 0;
-            return;
+    auto open_run = [&]() {  // the first segment from f on in which this warp has k-blocks
+        while (f.nrows) {
+            int beg, end;
+            run_of(f, warp, &beg, &end);
+            f_left = end - beg;
+            if (f_left > 0) {
+                const uint8_t* we = a.wp + static_cast<size_t>(f.e) * a.expert_stride;
+                const int u = f.u0 + beg / KT;
+                f_kb = beg % KT;
+                f_codes = we + (static_cast<size_t>(u) * KT + f_kb) * kExUnitBytes + lane * 16;
+                f_scales = we + a.scale_offset + static_cast<size_t>(u) * G * (kExUnitN * 2) + gc * 8;
+                return;
+            }
+            f = after(f);
         }
-        const uint8_t* we = a.wp + static_cast<size_t>(next.e) * a.expert_stride;
-        f_codes = we + (static_cast<size_t>(next.ct) * KT + f_kb) * kExUnitBytes + lane * 16;
-        f_scales = we + a.scale_offset + static_cast<size_t>(next.ct) * (a.K / a.g) * (kExUnitN * 2) + gc * 8;
+        f_left = 0;
+    };
+    auto fetch = [&]() {
+        if (f_left == 0) return;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = ldg_stream16(f_codes + i * 512);
+        f_codes += kExUnitBytes;
+        if (SL) {
+#pragma unroll
+            for (int i = 0; i < kS; ++i) {
+                const int grp = SL == 1 ? (kb_per_group == 1 ? f_kb : f_kb / kb_per_group) : f_kb * SL + i;
+                sc[i] = __ldg(reinterpret_cast<const uint2*>(f_scales + static_cast<size_t>(grp) * (kExUnitN * 2)));
+            }
+        }
+        if (++f_kb == KT) {
+            f_kb = 0;
+            f_scales += static_cast<size_t>(G) * (kExUnitN * 2);
+        }
+        if (--f_left == 0) {
+            f = after(f);
+            open_run();
+        }
+    };
+
+    // ---- the rows of a segment, in the order in which ldmatrix takes them: [K / 8][8 rows] 16 bytes
+    auto load_rows = [&](const Segment& s, int place) {
+        if (s.nrows == 0) return;
+        uint8_t* dst = s_rows + (places == 2 ? place : 0) * rows_bytes;
+        const int r = lane & 7, piece = lane >> 3;  // four pieces of a row, eight rows
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            const bool in = b * 8 + gc < next.nrows;
-            const bool good = static_cast<unsigned>(place[b]) < static_cast<unsigned>(a.pairs);
-            arow[b] = in && good ? a.a + static_cast<size_t>(row_of_pair(place[b], a)) * a.K + q * 8 : nullptr;
-            if (in && !good) atomicCAS(a.status, 0, 1 /* WQ_ERR_INVALID_ARG */);
-            if (q == 0) q_entry.pair[b * 8 + gc] = in && good ? place[b] : -1;
+            const int row = b * 8 + r;
+            if (row >= s.nrows) continue;  // what lies there meets no stored sum
+            const int p = __ldg(a.rows + s.row0 + row);
+            const bool good = static_cast<unsigned>(p) < static_cast<unsigned>(a.pairs);
+            if (!good) atomicCAS(a.status, 0, 1 /* WQ_ERR_INVALID_ARG */);
+            if (warp == 0 && piece == 0) s_pair[place][row] = good ? p : -1;
+            const uint16_t* src = a.a + static_cast<size_t>(good ? row_of_pair(p, a) : 0) * a.K;
+            for (int c = warp * 4 + piece; c < a.K / 8; c += W * 4)
+                cp_async16(dst + (static_cast<size_t>(b) * (a.K / 8) + c) * 128 + r * 16, src + c * 8);
         }
-        if (lane == 0) {
-            q_entry.e = next.e;
-            q_entry.ct = next.ct;
-            q_entry.nrows = next.nrows;
-        }
-        next.next();
-        read_rows();
     };
-    // load this warp's next k-block into slot d (compile-time): codes, scales, activations
-    auto fetch = [&](int d) {
-        if (f_valid) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[d][i] = ldg_stream16(f_codes + i * 512);
-            f_codes += WK * kExUnitBytes;
-            if (SL) {
-#pragma unroll
-                for (int i = 0; i < kS; ++i) {
-                    const int grp = SL == 1 ? (kb_per_group == 1 ? f_kb : f_kb / kb_per_group) : f_kb * SL + i;
-                    sc[d][i] = __ldg(reinterpret_cast<const uint2*>(f_scales + static_cast<size_t>(grp) * (kExUnitN * 2)));
-                }
+
+    open_run();
+    Segment s = segment_at(tile0, 0);
+    if (s.nrows == 0) return;
+    fetch();
+    load_rows(s, 0);
+    cp_async_commit();
+    int place = 0;
+    float* mine = sums + warp * 2 * C::kSums;
+
+    // Columns of lane's output in column tile u: value of a row from sums already added up.
+    auto store_rows = [&](int u, const Segment& g, auto&& value) {
+        const uint8_t* we = a.wp + static_cast<size_t>(g.e) * a.expert_stride;
+        const __half* cs = reinterpret_cast<const __half*>(we + a.scale_offset) + static_cast<size_t>(u) * kExUnitN;
+        if (a.gated) {
+            const int col = lane & 15, v0 = (col >> 3) * 16 + (col & 7), n = u * 16 + col;
+            float c0 = 1.f, c1 = 1.f;
+            if (SL == 0) {
+                const int at = (v0 & 7) * 4 + (v0 >> 4) * 2;
+                c0 = __half2float(cs[at]);
+                c1 = __half2float(cs[at + 1]);
             }
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-                if (arow[b]) {
-                    // rows behind the tile's last are not copied: what lies there meets no stored sum
-                    uint8_t* dst = ring + (d * NB + b) * 2048 + q * 128 + gc * 16;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) cp_async16(dst + c * 512, arow[b] + f_kb * kTileK + c * 32);
-                }
-            f_kb += WK;
-            if (f_kb >= KT) {
-                f_kb = ks;
-                open_tile();
+            for (int m = lane >> 4; m < g.nrows; m += 2) {
+                const float out = silu_mul(value(m, v0) * c0, value(m, v0 + 8) * c1);
+                const int p = s_pair[place][m];
+                if (n < n_out && p >= 0) a.y[static_cast<size_t>(p) * n_out + n] = __half_as_ushort(__float2half_rn(out));
+            }
+        } else {
+            const int n = u * kExUnitN + lane;
+            float c0 = 1.f;
+            if (SL == 0) c0 = __half2float(cs[(lane & 7) * 4 + (lane >> 4) * 2 + ((lane >> 3) & 1)]);
+            for (int m = 0; m < g.nrows; ++m) {
+                const float out = value(m, lane) * c0;
+                const int p = s_pair[place][m];
+                if (n < n_out && p >= 0) a.y[static_cast<size_t>(p) * n_out + n] = __half_as_ushort(__float2half_rn(out));
             }
         }
-        cp_async_commit();
     };
-    open_tile();
-#pragma unroll
-    for (int d = 0; d < D; ++d) fetch(d);
 
     float acc[2][NB][4];
 #pragma unroll
@@ -177,30 +231,20 @@ __global__ void __launch_bounds__(C::W * 32, 1) experts_kernel(ExpertArgs a, int
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[r][b][i] = 0.f;
-    int kb = ks, at = 0, turn = 0;
-    __syncwarp();
-    const Entry* t = &s_queue[warp][0];  // the tile that is summed
-    int nrows = t->nrows;
-    float cs0 = 1.f, cs1 = 1.f;  // column scales of this lane's output, g == K
-    auto column_scales = [&]() {
-        if (SL == 0 && nrows) {
-            const uint8_t* we = a.wp + static_cast<size_t>(t->e) * a.expert_stride;
-            const __half* cs = reinterpret_cast<const __half*>(we + a.scale_offset) + static_cast<size_t>(t->ct) * kExUnitN;
-            const int v0 = a.gated ? ((lane >> 3) & 1) * 16 + (lane & 7) : lane;
-            const int place = (v0 & 7) * 4 + (v0 >> 4) * 2 + ((v0 >> 3) & 1);
-            cs0 = __half2float(cs[place]);
-            if (a.gated) cs1 = __half2float(cs[place + 1]);
-        }
-    };
-    column_scales();
-    while (nrows) {
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-            if (!nrows) break;
-            cp_async_wait<D - 1>();
-            __syncwarp();
-            const uint8_t* st = ring + d * NB * 2048 + lane * 16;
-            float s[2][NB][4];
+    while (s.nrows) {
+        const Segment next = after(s);
+        cp_async_wait<0>();
+        __syncthreads();  // this segment's rows are there, and the last one's sums and pairs are read
+        if (places == 2) load_rows(next, place ^ 1);
+        cp_async_commit();
+        int beg, end;
+        run_of(s, warp, &beg, &end);
+        const uint8_t* rows0 = s_rows + (places == 2 ? place : 0) * rows_bytes + lane * 16;
+        int kb = beg % KT, u = s.u0 + beg / KT;
+        bool whole = kb == 0, first = true;  // the piece of tile u that this warp is on
+        for (int unit = beg; unit < end;) {
+            const uint8_t* st = rows0 + static_cast<size_t>(kb) * 2048;
+            float t[2][NB][4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 constexpr int kPer = SL ? 4 / kS : 4;  // 32-row blocks of a scale
@@ -210,114 +254,114 @@ __global__ void __launch_bounds__(C::W * 32, 1) experts_kernel(ExpertArgs a, int
 #pragma unroll
                         for (int b = 0; b < NB; ++b)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) s[r][b][i] = 0.f;
+                            for (int i = 0; i < 4; ++i) t[r][b][i] = 0.f;
                 }
                 uint4 x[NB];
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
-                    if (b == 0 || b * 8 < nrows) x[b] = ldmatrix4(st + b * 2048 + c * 512);
+                    if (b == 0 || b * 8 < s.nrows) x[b] = ldmatrix4(st + static_cast<size_t>(b) * a.K * 16 + c * 512);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     uint32_t p0[4], p1[4];
-                    const uint4 w0 = w[d][2 * r], w1 = w[d][2 * r + 1];
+                    const uint4 w0 = w[2 * r], w1 = w[2 * r + 1];
                     dequant8(c == 0 ? w0.x : c == 1 ? w0.y : c == 2 ? w0.z : w0.w, p0);
                     dequant8(c == 0 ? w1.x : c == 1 ? w1.y : c == 2 ? w1.z : w1.w, p1);
 #pragma unroll
                     for (int b = 0; b < NB; ++b)
-                        if (b == 0 || b * 8 < nrows) {
-                            float(&u)[4] = SL ? s[r][b] : acc[r][b];
-                            mma_16816(u, p0[0], p1[0], p0[1], p1[1], x[b].x, x[b].y);
-                            mma_16816(u, p0[2], p1[2], p0[3], p1[3], x[b].z, x[b].w);
+                        if (b == 0 || b * 8 < s.nrows) {
+                            float(&v)[4] = SL ? t[r][b] : acc[r][b];
+                            mma_16816(v, p0[0], p1[0], p0[1], p1[1], x[b].x, x[b].y);
+                            mma_16816(v, p0[2], p1[2], p0[3], p1[3], x[b].z, x[b].w);
                         }
                 }
                 if (SL && c % kPer == kPer - 1) {
-                    const uint2 sv = sc[d][c / kPer];
+                    const uint2 sv = sc[c / kPer];
                     const float2 s0 = __half22float2(*reinterpret_cast<const __half2*>(&sv.x));
                     const float2 s1 = __half22float2(*reinterpret_cast<const __half2*>(&sv.y));
 #pragma unroll
                     for (int b = 0; b < NB; ++b)
-                        if (b == 0 || b * 8 < nrows) {
-                            acc[0][b][0] += s0.x * s[0][b][0];
-                            acc[0][b][1] += s0.x * s[0][b][1];
-                            acc[0][b][2] += s0.y * s[0][b][2];
-                            acc[0][b][3] += s0.y * s[0][b][3];
-                            acc[1][b][0] += s1.x * s[1][b][0];
-                            acc[1][b][1] += s1.x * s[1][b][1];
-                            acc[1][b][2] += s1.y * s[1][b][2];
-                            acc[1][b][3] += s1.y * s[1][b][3];
+                        if (b == 0 || b * 8 < s.nrows) {
+                            acc[0][b][0] += s0.x * t[0][b][0];
+                            acc[0][b][1] += s0.x * t[0][b][1];
+                            acc[0][b][2] += s0.y * t[0][b][2];
+                            acc[0][b][3] += s0.y * t[0][b][3];
+                            acc[1][b][0] += s1.x * t[1][b][0];
+                            acc[1][b][1] += s1.x * t[1][b][1];
+                            acc[1][b][2] += s1.y * t[1][b][2];
+                            acc[1][b][3] += s1.y * t[1][b][3];
                         }
                 }
             }
-            fetch(d);
-            kb += WK;
-            if (kb < KT) continue;
-
-            // the tile's end: sums of the group's warps, [warp][row][column]
-            float* sums = red + turn * (C::W * C::kRed / 4);
-            turn ^= 1;
-            float* mine = sums + ks * (C::kRed / 4);
+            fetch();
+            ++unit;
+            if (++kb < KT && unit < end) continue;
+            // the piece's end: a whole tile is stored, a part is left for the tile's first warp
+            const bool done = whole && kb == KT;
+            float* part = mine + (first && !done ? 0 : C::kSums);
+            __syncwarp();
 #pragma unroll
             for (int r = 0; r < 2; ++r)
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        mine[(b * 8 + 2 * q + (i & 1)) * C::kRedRow + r * 16 + (i >> 1) * 8 + gc] = acc[r][b][i];
+                        part[(b * 8 + 2 * q + (i & 1)) * C::kSumRow + r * 16 + (i >> 1) * 8 + gc] = acc[r][b][i];
                         acc[r][b][i] = 0.f;
                     }
-            // one barrier a tile: the sums of the next one go to the other buffer
-            if (WK > 1) named_barrier_sync(1 + group, WK * 32); else __syncwarp();
-            if (a.gated) {
-                const int col = lane & 15, v0 = (col >> 3) * 16 + (col & 7), n = t->ct * 16 + col;
-                for (int m = ks * 2 + (lane >> 4); m < nrows; m += WK * 2) {
-                    float gate = 0.f, up = 0.f;
-                    for (int k = 0; k < WK; ++k) {
-                        gate += sums[k * (C::kRed / 4) + m * C::kRedRow + v0];
-                        up += sums[k * (C::kRed / 4) + m * C::kRedRow + v0 + 8];
-                    }
-                    const int p = t->pair[m];
-                    const float out = silu_mul(gate * cs0, up * cs1);
-                    if (n < n_out && p >= 0) a.y[static_cast<size_t>(p) * n_out + n] = __half_as_ushort(__float2half_rn(out));
-                }
-            } else {
-                const int n = t->ct * 32 + lane;
-                for (int m = ks; m < nrows; m += WK) {
-                    float out = 0.f;
-                    for (int k = 0; k < WK; ++k) out += sums[k * (C::kRed / 4) + m * C::kRedRow + lane];
-                    const int p = t->pair[m];
-                    if (n < n_out && p >= 0) a.y[static_cast<size_t>(p) * n_out + n] = __half_as_ushort(__float2half_rn(out * cs0));
-                }
-            }
-            kb = ks;
-            at = at + 1 == C::kQueue ? 0 : at + 1;
             __syncwarp();
-            t = &s_queue[warp][at];
-            nrows = t->nrows;
-            column_scales();
+            if (done) store_rows(u, s, [&](int m, int v) { return part[m * C::kSumRow + v]; });
+            first = false;
+            whole = true;
+            kb = 0;
+            ++u;
         }
+        __syncthreads();  // all parts are there, the rows have been read
+        if (places == 1) load_rows(next, place ^ 1);
+        cp_async_commit();
+        if (beg < end) {
+            // a tile that begins in this warp's run and ends behind it
+            const int per = ((s.u1 - s.u0) * KT + W - 1) / W;
+            const int ut = (end - 1) / KT, tile_beg = ut * KT, tile_end = tile_beg + KT;
+            if (tile_beg >= beg && tile_end > end) {
+                const float* own = mine + (tile_beg == beg ? 0 : C::kSums);
+                const int last = (tile_end - 1) / per;  // warp with its last k-block
+                store_rows(s.u0 + ut, s, [&](int m, int v) {
+                    float sum = own[m * C::kSumRow + v];
+                    for (int k = warp + 1; k <= last; ++k) sum += sums[k * 2 * C::kSums + m * C::kSumRow + v];
+                    return sum;
+                });
+            }
+        }
+        s = next;
+        place ^= 1;
     }
     cp_async_wait<0>();
 }
 
-// The combined down product of a few tokens, without lists: a tile is 32 columns of one token's sum
-// over its experts, top_k * K long, whose 128-row k-blocks a group of WK warps takes in turn. A
-// weight's k-block is scaled by its group scale and the choice's weight together, in fp32. Experts
-// that two tokens share are read twice (the second time from L2), which is what limits this form to
-// few pairs; what it saves is a launch, the pairs' sums through memory and a rounding of each.
-template <int SL>
+// Few pairs: one row at a time, without a table of tiles. A tile is 32 columns of one row's product,
+// whose 128-row k-blocks a group of WK warps takes in turn, loading three ahead, across tiles.
+// kSum: the combined down product of a few tokens, without lists: the tile is a token's sum over its
+// experts, top_k * K long; a k-block is scaled by its group scale and the choice's weight together,
+// in fp32. It saves a launch, the pairs' sums through memory and a rounding of each. Otherwise row i
+// is place i of the lists; its expert ends at the first offset above i.
+// An expert that two rows share is read twice (the second time from L2), which is what limits this
+// form to few pairs.
+template <int SL, bool kSum>
 __global__ void __launch_bounds__(512, 1) experts_token_kernel(ExpertArgs a, const int32_t* __restrict__ idx,
                                                                const float* __restrict__ wt, int top_k, int WK) {
     constexpr int W = 16, D = SL == 4 ? 2 : 3;
     __shared__ __align__(16) uint8_t s_ring[W][D][256];  // the token's row of a k-block
     __shared__ float s_sums[2][W][32];
+    __shared__ int s_out[W][D + 2];  // rows of Y of the open tiles, -1: none
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int q = lane & 3, gc = lane >> 2;
     const int group = warp / WK, ks = warp % WK, groups = W / WK;
     const int KT = a.K / kTileK, NU = ex_units(a.N);
-    const int units = top_k * KT;
+    const int n_out = a.gated ? a.N / 2 : a.N;
+    const int units = kSum ? top_k * KT : KT;
     const int G = a.K / a.g;                                     // groups along K (1: per-column scales)
     const int kb_per_group = SL == 1 && G > 1 ? a.g / kTileK : KT;
-    const unsigned tokens = a.pairs / top_k;
+    const unsigned tokens = kSum ? a.pairs / top_k : a.pairs;  // rows of the product
     const unsigned step = gridDim.x * groups, step_t = step / NU, step_u = step % NU;
 
     uint4 w[D][4];
@@ -326,20 +370,45 @@ __global__ void __launch_bounds__(512, 1) experts_token_kernel(ExpertArgs a, con
     unsigned good = 0;  // bit d: slot d holds a k-block of an expert
     // the tile that is loaded; lane j has its j-th choice
     unsigned f_t = (blockIdx.x * groups + group) / NU, f_u = (blockIdx.x * groups + group) % NU;
-    int f_unit = ks, my_e = -1;
-    float my_w = 0.f;
+    int f_unit = ks, f_at = 0, my_e = -1;
+    float my_w = 1.f;
+    const uint16_t* f_row = a.a;
     auto open_tile = [&]() {
-        if (f_t < tokens && lane < top_k) {
-            const size_t p = static_cast<size_t>(f_t) * top_k + lane;
-            my_e = __ldg(idx + p);
-            my_w = __ldg(wt + p);
+        if (f_t >= tokens) return;
+        int out = static_cast<int>(f_t);
+        if (kSum) {
+            if (lane < top_k) {
+                const size_t p = static_cast<size_t>(f_t) * top_k + lane;
+                my_e = __ldg(idx + p);
+                my_w = __ldg(wt + p);
+            }
+            f_row = a.a + static_cast<size_t>(f_t) * top_k * a.K;
+        } else {
+            const int p = __ldg(a.rows + f_t);
+            // the first offset above the row's place ends its expert; none, or the very first: no expert
+            unsigned ends = a.E + 1;
+#pragma unroll 4
+            for (int e = lane; e <= a.E; e += 32)
+                if (__ldg(a.offsets + e) > static_cast<int>(f_t)) ends = min(ends, static_cast<unsigned>(e));
+            ends = __reduce_min_sync(kFull, ends);
+            my_e = ends == 0 ? a.E : static_cast<int>(ends) - 1;
+            out = -1;
+            if (static_cast<unsigned>(p) < static_cast<unsigned>(a.pairs)) {
+                out = my_e < a.E ? p : -1;
+                f_row = a.a + static_cast<size_t>(row_of_pair(p, a)) * a.K;
+            } else if (my_e < a.E) {
+                atomicCAS(a.status, 0, 1 /* WQ_ERR_INVALID_ARG */);
+                my_e = a.E;
+            }
         }
+        if (lane == 0) s_out[warp][f_at] = out;
+        f_at = f_at + 1 == D + 2 ? 0 : f_at + 1;
     };
     auto fetch = [&](int d) {
         if (f_t < tokens) {
-            const int j = f_unit / KT, kb = f_unit - j * KT;
-            const int e = __shfl_sync(kFull, my_e, j);
-            wj[d] = __shfl_sync(kFull, my_w, j);
+            const int j = kSum ? f_unit / KT : 0, kb = f_unit - j * KT;
+            const int e = kSum ? __shfl_sync(kFull, my_e, j) : my_e;
+            wj[d] = kSum ? __shfl_sync(kFull, my_w, j) : 1.f;
             good &= ~(1u << d);
             if (static_cast<unsigned>(e) < static_cast<unsigned>(a.E)) {  // else the choice adds nothing
                 good |= 1u << d;
@@ -354,8 +423,7 @@ __global__ void __launch_bounds__(512, 1) experts_token_kernel(ExpertArgs a, con
                         we + a.scale_offset + (static_cast<size_t>(f_u) * G + grp) * (kExUnitN * 2) + gc * 8));
                 }
                 if (lane < 16)
-                    cp_async16(&s_ring[warp][d][lane * 16],
-                               a.a + (static_cast<size_t>(f_t) * top_k + j) * a.K + kb * kTileK + lane * 8);
+                    cp_async16(&s_ring[warp][d][lane * 16], f_row + static_cast<size_t>(j) * a.K + kb * kTileK + lane * 8);
             }
             f_unit += WK;
             if (f_unit >= units) {
@@ -376,7 +444,7 @@ __global__ void __launch_bounds__(512, 1) experts_token_kernel(ExpertArgs a, con
 #pragma unroll
     for (int d = 0; d < D; ++d) fetch(d);
     float acc[2][2] = {};  // columns (rt, h) of lane gc; every quad lane holds the same
-    int unit = ks, turn = 0;
+    int unit = ks, turn = 0, at = 0;
     while (t < tokens) {
 #pragma unroll
         for (int d = 0; d < D; ++d) {
@@ -432,11 +500,19 @@ __global__ void __launch_bounds__(512, 1) experts_token_kernel(ExpertArgs a, con
 #pragma unroll
             for (int r = 0; r < 2; ++r) acc[r][0] = acc[r][1] = 0.f;
             if (WK > 1) named_barrier_sync(1 + group, WK * 32); else __syncwarp();
-            if (ks == 0) {
+            const int row = s_out[warp][at];
+            at = at + 1 == D + 2 ? 0 : at + 1;
+            if (ks == 0 && row >= 0) {
                 float out = 0.f;
                 for (int k = 0; k < WK; ++k) out += sums[k][lane];
-                const int n = u * kExUnitN + lane;
-                if (n < a.N) a.y[static_cast<size_t>(t) * a.N + n] = __half_as_ushort(__float2half_rn(out));
+                int n = u * kExUnitN + lane;
+                bool here = true;
+                if (!kSum && a.gated) {  // gate lanes take the up lane's sum
+                    out = silu_mul(out, __shfl_down_sync(kFull, out, 8));
+                    here = !(lane & 8);
+                    n = u * 16 + (lane >> 4) * 8 + (lane & 7);
+                }
+                if (here && n < n_out) a.y[static_cast<size_t>(row) * n_out + n] = __half_as_ushort(__float2half_rn(out));
             }
             unit = ks;
             t += step_t;
@@ -481,10 +557,9 @@ __global__ void __launch_bounds__(256) combine_kernel(const uint16_t* __restrict
     *reinterpret_cast<uint4*>(Y + t * N + n) = out;
 }
 
-template <int NB, int SL>
+template <class C>
 cudaError_t configure_small() {
-    using C = Small<NB, SL>;
-    return cudaFuncSetAttribute(experts_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    return cudaFuncSetAttribute(experts_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kMost));
 }
 
 // Warps per tile: the count that gives the busiest warp the fewest k-blocks, a tile's end counted as one.
@@ -502,41 +577,56 @@ int warps_per_tile(long long tiles, int k_blocks, int warps, int num_sms) {
     return best;
 }
 
-template <int NB, int SL>
+template <class C>
 cudaError_t launch_small(const ExpertArgs& a, int num_sms, cudaStream_t st) {
-    using C = Small<NB, SL>;
-    // the lists are on the device: taken to be spread over as many experts as there are pairs
-    const long long experts = a.pairs < a.E ? a.pairs : a.E;
-    const long long per = (a.pairs + experts - 1) / experts;
-    const long long tiles = experts * ((per + C::kRows - 1) / C::kRows) * ex_units(a.N);
-    const int best = warps_per_tile(tiles, a.K / kTileK, C::W, num_sms);
-    experts_kernel<C><<<num_sms, C::W * 32, C::kSmem, st>>>(a, best);
+    const int places = C::places(a.K);
+    experts_kernel<C><<<num_sms, C::W * 32, C::smem(a.K, places), st>>>(a, places);
     return cudaGetLastError();
 }
 
-template <int NB>
+template <int NB, int W>
 cudaError_t configure_nb() {
-    cudaError_t e = configure_small<NB, 0>();
-    if (e == cudaSuccess) e = configure_small<NB, 1>();
-    if (e == cudaSuccess) e = configure_small<NB, 2>();
-    if (e == cudaSuccess) e = configure_small<NB, 4>();
+    cudaError_t e = configure_small<Small<NB, 0, W>>();
+    if (e == cudaSuccess) e = configure_small<Small<NB, 1, W>>();
+    if (e == cudaSuccess) e = configure_small<Small<NB, 2, W>>();
+    if (e == cudaSuccess) e = configure_small<Small<NB, 4, W>>();
     return e;
 }
 
-template <int NB>
+template <int NB, int W>
 cudaError_t launch_nb(const ExpertArgs& a, int num_sms, cudaStream_t st) {
-    if (a.g == a.K) return launch_small<NB, 0>(a, num_sms, st);
-    if (a.g == 64) return launch_small<NB, 2>(a, num_sms, st);
-    if (a.g == 32) return launch_small<NB, 4>(a, num_sms, st);
-    return launch_small<NB, 1>(a, num_sms, st);
+    if (a.g == a.K) return launch_small<Small<NB, 0, W>>(a, num_sms, st);
+    if (a.g == 64) return launch_small<Small<NB, 2, W>>(a, num_sms, st);
+    if (a.g == 32) return launch_small<Small<NB, 4, W>>(a, num_sms, st);
+    return launch_small<Small<NB, 1, W>>(a, num_sms, st);
+}
+
+template <bool kSum>
+cudaError_t launch_token(const ExpertArgs& a, const int32_t* idx, const float* w, int top_k, int num_sms,
+                         cudaStream_t st) {
+    const long long tiles = static_cast<long long>(kSum ? a.pairs / top_k : a.pairs) * ex_units(a.N);
+    const int wk = warps_per_tile(tiles, (kSum ? top_k : 1) * (a.K / kTileK), 16, num_sms);
+    const long long ctas = (tiles + 16 / wk - 1) / (16 / wk);
+    const unsigned grid = static_cast<unsigned>(ctas < num_sms ? ctas : num_sms);
+    if (a.g == 64) experts_token_kernel<2, kSum><<<grid, 512, 0, st>>>(a, idx, w, top_k, wk);
+    else if (a.g == 32) experts_token_kernel<4, kSum><<<grid, 512, 0, st>>>(a, idx, w, top_k, wk);
+    else experts_token_kernel<1, kSum><<<grid, 512, 0, st>>>(a, idx, w, top_k, wk);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
+bool experts_token_form(int pairs, int E) { return pairs <= E / 4; }
+
+cudaError_t launch_experts_token(const ExpertArgs& a, const int32_t* idx, const float* w, int top_k, int num_sms,
+                                 cudaStream_t st) {
+    return launch_token<true>(a, idx, w, top_k, num_sms, st);
+}
+
 cudaError_t configure_expert_kernels() {
-    cudaError_t e = configure_nb<1>();
-    if (e == cudaSuccess) e = configure_nb<2>();
-    if (e == cudaSuccess) e = configure_nb<4>();
+    cudaError_t e = configure_nb<1, 24>();
+    if (e == cudaSuccess) e = configure_nb<1, 16>();
+    if (e == cudaSuccess) e = configure_nb<2, 16>();
     if (e == cudaSuccess) e = configure_experts_large();
     if (e == cudaSuccess) e = configure_route();
     return e;
@@ -544,25 +634,12 @@ cudaError_t configure_expert_kernels() {
 
 cudaError_t launch_experts(const ExpertArgs& a, const DeviceInfo& d, cudaStream_t st) {
     const long long per_expert = (static_cast<long long>(a.pairs) + a.E - 1) / a.E;
-    const int num_sms = d.num_sms;
-    if (per_expert > 16) return launch_experts_large(a, d, st);
-    if (per_expert <= 4) return launch_nb<1>(a, num_sms, st);
-    if (per_expert <= 8) return launch_nb<2>(a, num_sms, st);
-    return launch_nb<4>(a, num_sms, st);
-}
-
-bool experts_token_form(int pairs, int E) { return pairs <= E / 4; }
-
-cudaError_t launch_experts_token(const ExpertArgs& a, const int32_t* idx, const float* w, int top_k, int num_sms,
-                                 cudaStream_t st) {
-    const long long tiles = static_cast<long long>(a.pairs / top_k) * ex_units(a.N);
-    const int wk = warps_per_tile(tiles, top_k * (a.K / kTileK), 16, num_sms);
-    const long long ctas = (tiles + 16 / wk - 1) / (16 / wk);
-    const unsigned grid = static_cast<unsigned>(ctas < num_sms ? ctas : num_sms);
-    if (a.g == 64) experts_token_kernel<2><<<grid, 512, 0, st>>>(a, idx, w, top_k, wk);
-    else if (a.g == 32) experts_token_kernel<4><<<grid, 512, 0, st>>>(a, idx, w, top_k, wk);
-    else experts_token_kernel<1><<<grid, 512, 0, st>>>(a, idx, w, top_k, wk);
-    return cudaGetLastError();
+    if (experts_token_form(a.pairs, a.E)) return launch_token<false>(a, nullptr, nullptr, 1, d.num_sms, st);
+    // rows of 16 warps' places reach further than those of 24: K up to 11008 against 9728
+    if (per_expert > 16 || Small<1, 0, 16>::places(a.K) == 0) return launch_experts_large(a, d, st);
+    if (per_expert > 8 && Small<2, 0, 16>::places(a.K)) return launch_nb<2, 16>(a, d.num_sms, st);
+    if (Small<1, 0, 24>::places(a.K)) return launch_nb<1, 24>(a, d.num_sms, st);
+    return launch_nb<1, 16>(a, d.num_sms, st);
 }
 
 cudaError_t launch_combine_experts(const uint16_t* yp, const int32_t* idx, const float* w, int T, int top_k, int E,

@@ -194,6 +194,10 @@ PRODUCTS = [
     (16, 512, 80, 512, 4, 1, 0, 0),
     (40, 1280, 72, 640, 5, 2, 0, 0.4),
     (1024, 128, 8, 128, 200, 1, 0, 0.1),
+    # rows too long for two, or for one, of their places in shared memory
+    (3, 11008, 72, 128, 5, 2, 0, 0),
+    (4, 8192, 48, 64, 9, 3, 1, 0.2),
+    (2, 16384, 48, 128, 3, 2, 0, 0),
 ]
 
 
