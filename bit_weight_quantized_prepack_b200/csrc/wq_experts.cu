@@ -2,8 +2,8 @@
 // W = (q - 8) * s, fp32 sums, one rounding to fp16; gated: silu(gate) * up in the epilogue.
 // And the weighted sum of a token's pairs after the down product.
 //
-// experts_kernel (few rows per expert). Tile: 32 columns of one expert x up to 8*NB of its rows, all
-// of K. A CTA has an equal run of all tiles, as segments of one row tile each, whose rows it keeps
+// experts_kernel (few rows per expert). Tile: 32 columns of one expert x up to 8 of its rows, all of
+// K. A CTA has an equal run of all tiles, as segments of one row tile each, whose rows it keeps
 // in shared memory. Each of its 16 warps has an equal run of a segment's k-blocks (tile after tile,
 // 2 KiB of codes each, contiguous in memory) and streams them, across segments, into registers: 16
 // bytes a lane, a whole fragment of the weight. The weight is the 16-row operand of m16n8k16 (exact
@@ -54,13 +54,12 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// NB: blocks of 8 rows. SL: scales per k-block and column (1, 2 or 4 groups of a k-block; 0:
-// per-column, g == K). W: warps. With one k-block ahead of the one in hand, 24 warps of 80 registers
+// SL: scales per k-block and column (1, 2 or 4 groups of a k-block; 0: per-column, g == K). W: warps. With one k-block ahead of the one in hand, 24 warps of 80 registers
 // hide more than 16 of 128 with three (up_wide 72.6 us against 84.4; 28 warps 74.6, 32 76.5).
-template <int NB_, int SL_, int W_>
+template <int SL_, int W_>
 struct Small {
-    static constexpr int NB = NB_, SL = SL_, W = W_;
-    static constexpr int kRows = 8 * NB;
+    static constexpr int SL = SL_, W = W_;
+    static constexpr int kRows = 8;
     static constexpr int kSumRow = 36;                     // floats of a row of sums, with padding
     static constexpr int kSums = kRows * kSumRow;          // floats of a tile's sums
     static constexpr size_t rows_bytes(int K) { return static_cast<size_t>(kRows) * K * 2; }
@@ -73,7 +72,7 @@ struct Small {
 
 template <class C>
 __global__ void __launch_bounds__(C::W * 32, 1) experts_kernel(ExpertArgs a, int places) {
-    constexpr int NB = C::NB, SL = C::SL, W = C::W, kS = SL ? SL : 1, kRows = C::kRows;
+    constexpr int SL = C::SL, W = C::W, kS = SL ? SL : 1, kRows = C::kRows;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     __shared__ int s_start[kExMaxExperts + 1], s_tiles[kExMaxExperts + 1], s_each[kExMaxExperts], s_scratch[W];
     __shared__ int s_pair[2][kRows];
@@ -171,19 +170,15 @@ __global__ void __launch_bounds__(C::W * 32, 1) experts_kernel(ExpertArgs a, int
     auto load_rows = [&](const Segment& s, int place) {
         if (s.nrows == 0) return;
         uint8_t* dst = s_rows + (places == 2 ? place : 0) * rows_bytes;
-        const int r = lane & 7, piece = lane >> 3;  // four pieces of a row, eight rows
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            const int row = b * 8 + r;
-            if (row >= s.nrows) continue;  // what lies there meets no stored sum
-            const int p = __ldg(a.rows + s.row0 + row);
-            const bool good = static_cast<unsigned>(p) < static_cast<unsigned>(a.pairs);
-            if (!good) atomicCAS(a.status, 0, 1 /* WQ_ERR_INVALID_ARG */);
-            if (warp == 0 && piece == 0) s_pair[place][row] = good ? p : -1;
-            const uint16_t* src = a.a + static_cast<size_t>(good ? row_of_pair(p, a) : 0) * a.K;
-            for (int c = warp * 4 + piece; c < a.K / 8; c += W * 4)
-                cp_async16(dst + (static_cast<size_t>(b) * (a.K / 8) + c) * 128 + r * 16, src + c * 8);
-        }
+        const int row = lane & 7, piece = lane >> 3;  // four pieces of a row, eight rows
+        if (row >= s.nrows) return;  // what lies there meets no stored sum
+        const int p = __ldg(a.rows + s.row0 + row);
+        const bool good = static_cast<unsigned>(p) < static_cast<unsigned>(a.pairs);
+        if (!good) atomicCAS(a.status, 0, 1 /* WQ_ERR_INVALID_ARG */);
+        if (warp == 0 && piece == 0) s_pair[place][row] = good ? p : -1;
+        const uint16_t* src = a.a + static_cast<size_t>(good ? row_of_pair(p, a) : 0) * a.K;
+        for (int c = warp * 4 + piece; c < a.K / 8; c += W * 4)
+            cp_async16(dst + static_cast<size_t>(c) * 128 + row * 16, src + c * 8);
     };
 
     open_run();
@@ -224,13 +219,11 @@ __global__ void __launch_bounds__(C::W * 32, 1) experts_kernel(ExpertArgs a, int
         }
     };
 
-    float acc[2][NB][4];
+    float acc[2][4];
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[r][b][i] = 0.f;
+        for (int i = 0; i < 4; ++i) acc[r][i] = 0.f;
     while (s.nrows) {
         const Segment next = after(s);
         cp_async_wait<0>();
@@ -244,7 +237,7 @@ __global__ void __launch_bounds__(C::W * 32, 1) experts_kernel(ExpertArgs a, int
         bool whole = kb == 0, first = true;  // the piece of tile u that this warp is on
         for (int unit = beg; unit < end;) {
             const uint8_t* st = rows0 + static_cast<size_t>(kb) * 2048;
-            float t[2][NB][4];
+            float t[2][4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 constexpr int kPer = SL ? 4 / kS : 4;  // 32-row blocks of a scale
@@ -252,44 +245,31 @@ __global__ void __launch_bounds__(C::W * 32, 1) experts_kernel(ExpertArgs a, int
 #pragma unroll
                     for (int r = 0; r < 2; ++r)
 #pragma unroll
-                        for (int b = 0; b < NB; ++b)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) t[r][b][i] = 0.f;
+                        for (int i = 0; i < 4; ++i) t[r][i] = 0.f;
                 }
-                uint4 x[NB];
-#pragma unroll
-                for (int b = 0; b < NB; ++b)
-                    if (b == 0 || b * 8 < s.nrows) x[b] = ldmatrix4(st + static_cast<size_t>(b) * a.K * 16 + c * 512);
+                const uint4 x = ldmatrix4(st + c * 512);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     uint32_t p0[4], p1[4];
                     const uint4 w0 = w[2 * r], w1 = w[2 * r + 1];
                     dequant8(c == 0 ? w0.x : c == 1 ? w0.y : c == 2 ? w0.z : w0.w, p0);
                     dequant8(c == 0 ? w1.x : c == 1 ? w1.y : c == 2 ? w1.z : w1.w, p1);
-#pragma unroll
-                    for (int b = 0; b < NB; ++b)
-                        if (b == 0 || b * 8 < s.nrows) {
-                            float(&v)[4] = SL ? t[r][b] : acc[r][b];
-                            mma_16816(v, p0[0], p1[0], p0[1], p1[1], x[b].x, x[b].y);
-                            mma_16816(v, p0[2], p1[2], p0[3], p1[3], x[b].z, x[b].w);
-                        }
+                    float(&v)[4] = SL ? t[r] : acc[r];
+                    mma_16816(v, p0[0], p1[0], p0[1], p1[1], x.x, x.y);
+                    mma_16816(v, p0[2], p1[2], p0[3], p1[3], x.z, x.w);
                 }
                 if (SL && c % kPer == kPer - 1) {
                     const uint2 sv = sc[c / kPer];
                     const float2 s0 = __half22float2(*reinterpret_cast<const __half2*>(&sv.x));
                     const float2 s1 = __half22float2(*reinterpret_cast<const __half2*>(&sv.y));
-#pragma unroll
-                    for (int b = 0; b < NB; ++b)
-                        if (b == 0 || b * 8 < s.nrows) {
-                            acc[0][b][0] += s0.x * t[0][b][0];
-                            acc[0][b][1] += s0.x * t[0][b][1];
-                            acc[0][b][2] += s0.y * t[0][b][2];
-                            acc[0][b][3] += s0.y * t[0][b][3];
-                            acc[1][b][0] += s1.x * t[1][b][0];
-                            acc[1][b][1] += s1.x * t[1][b][1];
-                            acc[1][b][2] += s1.y * t[1][b][2];
-                            acc[1][b][3] += s1.y * t[1][b][3];
-                        }
+                    acc[0][0] += s0.x * t[0][0];
+                    acc[0][1] += s0.x * t[0][1];
+                    acc[0][2] += s0.y * t[0][2];
+                    acc[0][3] += s0.y * t[0][3];
+                    acc[1][0] += s1.x * t[1][0];
+                    acc[1][1] += s1.x * t[1][1];
+                    acc[1][2] += s1.y * t[1][2];
+                    acc[1][3] += s1.y * t[1][3];
                 }
             }
             fetch();
@@ -302,12 +282,10 @@ __global__ void __launch_bounds__(C::W * 32, 1) experts_kernel(ExpertArgs a, int
 #pragma unroll
             for (int r = 0; r < 2; ++r)
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        part[(b * 8 + 2 * q + (i & 1)) * C::kSumRow + r * 16 + (i >> 1) * 8 + gc] = acc[r][b][i];
-                        acc[r][b][i] = 0.f;
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    part[(2 * q + (i & 1)) * C::kSumRow + r * 16 + (i >> 1) * 8 + gc] = acc[r][i];
+                    acc[r][i] = 0.f;
+                }
             __syncwarp();
             if (done) store_rows(u, s, [&](int m, int v) { return part[m * C::kSumRow + v]; });
             first = false;
@@ -527,7 +505,8 @@ __global__ void __launch_bounds__(512, 1) experts_token_kernel(ExpertArgs a, con
 }
 
 // Y[t] = sum over j of w[t, j] * yp[t * top_k + j], in the order of j, fp32; a choice outside
-// [0, E) adds nothing. One thread per 8 columns of a token.
+// [0, E) adds nothing and its row is not read. One thread per 8 columns of a token, four choices'
+// rows under way at a time. Bound by the pairs' bytes (down_prefill: 134 MB of pairs in 26 us).
 __global__ void __launch_bounds__(256) combine_kernel(const uint16_t* __restrict__ yp, const int32_t* __restrict__ idx,
                                                       const float* __restrict__ w, int top_k, int E, int N,
                                                       uint16_t* __restrict__ Y, long long total) {
@@ -535,19 +514,31 @@ __global__ void __launch_bounds__(256) combine_kernel(const uint16_t* __restrict
     if (i >= total) return;
     const int per_row = N / 8;
     const long long t = i / per_row;
-    const int n = static_cast<int>(i % per_row) * 8;
+    const int n = static_cast<int>(i - t * per_row) * 8;
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int j = 0; j < top_k; ++j) {
-        const long long p = t * top_k + j;
-        if (static_cast<unsigned>(__ldg(idx + p)) >= static_cast<unsigned>(E)) continue;
-        const float wj = __ldg(w + p);
-        const uint4 v = *reinterpret_cast<const uint4*>(yp + p * N + n);
-        const __half2* h = reinterpret_cast<const __half2*>(&v);
+    for (int j0 = 0; j0 < top_k; j0 += 4) {
+        uint4 v[4];
+        float wj[4];
+        bool in[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float2 f = __half22float2(h[k]);
-            acc[2 * k] += wj * f.x;
-            acc[2 * k + 1] += wj * f.y;
+        for (int j = 0; j < 4; ++j) {
+            const long long p = t * top_k + j0 + j;
+            in[j] = j0 + j < top_k && static_cast<unsigned>(__ldg(idx + p)) < static_cast<unsigned>(E);
+            wj[j] = in[j] ? __ldg(w + p) : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (in[j]) v[j] = ldg_stream16(yp + (t * top_k + j0 + j) * N + n);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (!in[j]) continue;
+            const __half2* h = reinterpret_cast<const __half2*>(&v[j]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 f = __half22float2(h[k]);
+                acc[2 * k] += wj[j] * f.x;
+                acc[2 * k + 1] += wj[j] * f.y;
+            }
         }
     }
     uint4 out;
@@ -584,21 +575,21 @@ cudaError_t launch_small(const ExpertArgs& a, int num_sms, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-template <int NB, int W>
-cudaError_t configure_nb() {
-    cudaError_t e = configure_small<Small<NB, 0, W>>();
-    if (e == cudaSuccess) e = configure_small<Small<NB, 1, W>>();
-    if (e == cudaSuccess) e = configure_small<Small<NB, 2, W>>();
-    if (e == cudaSuccess) e = configure_small<Small<NB, 4, W>>();
+template <int W>
+cudaError_t configure_w() {
+    cudaError_t e = configure_small<Small<0, W>>();
+    if (e == cudaSuccess) e = configure_small<Small<1, W>>();
+    if (e == cudaSuccess) e = configure_small<Small<2, W>>();
+    if (e == cudaSuccess) e = configure_small<Small<4, W>>();
     return e;
 }
 
-template <int NB, int W>
-cudaError_t launch_nb(const ExpertArgs& a, int num_sms, cudaStream_t st) {
-    if (a.g == a.K) return launch_small<Small<NB, 0, W>>(a, num_sms, st);
-    if (a.g == 64) return launch_small<Small<NB, 2, W>>(a, num_sms, st);
-    if (a.g == 32) return launch_small<Small<NB, 4, W>>(a, num_sms, st);
-    return launch_small<Small<NB, 1, W>>(a, num_sms, st);
+template <int W>
+cudaError_t launch_w(const ExpertArgs& a, int num_sms, cudaStream_t st) {
+    if (a.g == a.K) return launch_small<Small<0, W>>(a, num_sms, st);
+    if (a.g == 64) return launch_small<Small<2, W>>(a, num_sms, st);
+    if (a.g == 32) return launch_small<Small<4, W>>(a, num_sms, st);
+    return launch_small<Small<1, W>>(a, num_sms, st);
 }
 
 template <bool kSum>
@@ -624,22 +615,26 @@ cudaError_t launch_experts_token(const ExpertArgs& a, const int32_t* idx, const 
 }
 
 cudaError_t configure_expert_kernels() {
-    cudaError_t e = configure_nb<1, 24>();
-    if (e == cudaSuccess) e = configure_nb<1, 16>();
-    if (e == cudaSuccess) e = configure_nb<2, 16>();
+    cudaError_t e = configure_w<24>();
+    if (e == cudaSuccess) e = configure_w<16>();
     if (e == cudaSuccess) e = configure_experts_large();
     if (e == cudaSuccess) e = configure_route();
     return e;
 }
 
+// Rows per expert, were the pairs spread evenly, up to which mma.sync tiles of 8 rows beat the tcgen05
+// tiles, which need the same time up to some hundred rows. Measured at 8 / 12 / 16 rows: 64 experts of
+// 2048 x 2048 48.5 / 60.1 / 74.6 us against 58.6 / 58.7 / 59.0, 8 of 4096 x 8192 51.3 / 60.6 / 70.9
+// against 64.4 / 64.3 / 64.2.
+constexpr int kFewRows = 12;
+
 cudaError_t launch_experts(const ExpertArgs& a, const DeviceInfo& d, cudaStream_t st) {
     const long long per_expert = (static_cast<long long>(a.pairs) + a.E - 1) / a.E;
     if (experts_token_form(a.pairs, a.E)) return launch_token<false>(a, nullptr, nullptr, 1, d.num_sms, st);
     // rows of 16 warps' places reach further than those of 24: K up to 11008 against 9728
-    if (per_expert > 16 || Small<1, 0, 16>::places(a.K) == 0) return launch_experts_large(a, d, st);
-    if (per_expert > 8 && Small<2, 0, 16>::places(a.K)) return launch_nb<2, 16>(a, d.num_sms, st);
-    if (Small<1, 0, 24>::places(a.K)) return launch_nb<1, 24>(a, d.num_sms, st);
-    return launch_nb<1, 16>(a, d.num_sms, st);
+    if (per_expert > kFewRows || Small<0, 16>::places(a.K) == 0) return launch_experts_large(a, d, st);
+    if (Small<0, 24>::places(a.K)) return launch_w<24>(a, d.num_sms, st);
+    return launch_w<16>(a, d.num_sms, st);
 }
 
 cudaError_t launch_combine_experts(const uint16_t* yp, const int32_t* idx, const float* w, int T, int top_k, int E,

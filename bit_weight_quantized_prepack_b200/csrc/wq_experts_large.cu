@@ -30,16 +30,18 @@ namespace wq {
 
 namespace {
 
-constexpr int kLThreads = 16 * 32;
+constexpr int kDqTurns = 2;                        // a k-block in so many belongs to a dequant warp
+constexpr int kLThreads = (8 + 4 * kDqTurns) * 32;
 constexpr int kRowsMax = 192;                      // rows of a tile
 constexpr int kColsL = 128;                        // columns of a tile
 constexpr int kChunkK = 64;                        // weight rows of a stage: one 128-byte swizzle span
 constexpr int kHalfRows = kRowsMax / 2;            // rows of a tile that one CTA of the pair holds
-constexpr int kBBytes = kHalfRows * kChunkK * 2;   // 12 KiB
-constexpr int kStagesB = 16;
-constexpr int kSlotsA = 4;
+constexpr int kChunkBytes = kHalfRows * kChunkK * 2;  // 12 KiB
+constexpr int kStageBytes = 2 * kChunkBytes;       // a k-block: two chunks
+constexpr int kStages = 8;                         // k-blocks of rows in shared memory
+constexpr int kSlotsA = 2;                         // k-blocks of weights in tensor memory
 constexpr int kTmemA = 2 * kRowsMax;               // tensor-memory column of the weight slots
-constexpr int kSmemL = kStagesB * kBBytes + 1024;  // + alignment of the first stage
+constexpr int kSmemL = kStages * kStageBytes + 1024;  // + alignment of the first stage
 constexpr int kGatherWarps = 3, kMmaWarp = 3, kEpiWarp0 = 4, kDqWarp0 = 8;
 constexpr int kQuads = kHalfRows / 4;              // a warp's copy instruction takes four rows
 
@@ -47,7 +49,7 @@ constexpr int kYRow = 80, kYRowGated = 48;         // bytes of an output row on 
 constexpr int kYBytes = 32 * kYRow;
 
 struct Bars {
-    uint64_t full[kStagesB], empty[kStagesB];
+    uint64_t full[kStages], empty[kStages][2];  // empty: per chunk
     uint64_t acc_full[2], acc_empty[2], drain;
 };
 
@@ -64,7 +66,7 @@ struct Ctl {
 
 // Arrive on the leader's barrier that lies where `bar` lies in this CTA. What the leader's MMAs
 // read is ordered by the proxy and tcgen05 fences before it, not by this arrival: one that releases
-// at cluster scope costs its thread some hundred cycles (up_prefill 366 us against 213).
+// at cluster scope costs its thread some hundred cycles (up_prefill 366 us against 221).
 __device__ __forceinline__ void mbar_arrive_leader(uint64_t* bar) {
     asm volatile(
         "{\n\t.reg .b32 remote;\n\t"
@@ -84,6 +86,7 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 // Bounded wait for a phase; false when it expired or another role gave up.
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, const Ctl& c, bool honour_stop = true) {
     if (mbar_test_wait(bar, parity)) return true;
+    if (mbar_try_wait_sleep(bar, parity, 20000)) return true;  // the timer is read only by long waits
     const uint64_t t0 = global_timer_ns();
     while (true) {
         if (mbar_try_wait_sleep(bar, parity, 20000)) return true;
@@ -169,9 +172,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
     uint8_t* ring = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
 
     if (tid == 0) {
-        for (int i = 0; i < kStagesB; ++i) {
+        for (int i = 0; i < kStages; ++i) {
             mbar_init(&bars.full[i], 2 + 8);  // a gather warp and four dequant warps of each CTA
-            mbar_init(&bars.empty[i], 1);
+            mbar_init(&bars.empty[i][0], 1);
+            mbar_init(&bars.empty[i][1], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.acc_full[i], 1);
@@ -190,23 +194,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     const Ctl ctl{&s_stop, a.status, args.timeout_ns};
-    const int KT = a.K / kTileK, chunks = a.K / kChunkK;
+    const int KT = a.K / kTileK;
     const int CT = (a.N + 2 * kColsL - 1) / (2 * kColsL), NU = ex_units(a.N);
     // column tiles of the same rows are neighbours; pair b takes tiles b, b + pairs, ...
     Walk t(CT, a.E, blockIdx.x / 2, gridDim.x / 2, s_start, s_tiles, s_each);
 
     if (warp < kGatherWarps) {
         // ---------------------------------------------------------------- rows of the activations
-        // Warp w copies chunks w, w + 3, ... whole: lane l the 16-byte piece l % 8 of rows 4j + l / 8.
-        // It signals a chunk when the next of its own is under way.
+        // Warp w copies k-blocks w, w + 3, ... whole: lane l the 16-byte piece l % 8 of rows 4j + l / 8 of
+        // both chunks. It signals a k-block when the next of its own is under way.
         const int piece = lane & 7, sub = lane >> 3;
         // place of the piece in the swizzled row, for even and odd quads
         const uint32_t base = smem_addr(ring) + sub * 128;
         const uint32_t dst_even = base + ((piece ^ sub) << 4), dst_odd = base + ((piece ^ (4 + sub)) << 4);
         const unsigned row_bytes = static_cast<unsigned>(a.K) * 2;
-        unsigned n = 0;     // chunk
+        unsigned n = 0;     // k-block
         bool ok = true, pending = false;
-        unsigned last = 0;  // stage of the pending chunk
+        unsigned last = 0;  // stage of the pending one
         auto signal = [&]() {
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
@@ -241,20 +245,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
             t.next();
             more = !t.done();
             bool read = false;
-            // this warp's first chunk of the tile
-            for (int c = (warp + kGatherWarps - tile_n % kGatherWarps) % kGatherWarps; c < chunks; c += kGatherWarps) {
+            // this warp's first k-block of the tile
+            for (int c = (warp + kGatherWarps - tile_n % kGatherWarps) % kGatherWarps; c < KT; c += kGatherWarps) {
                 n = tile_n + c;
-                const unsigned stage = n % kStagesB;
-                ok = __all_sync(kFull, wait_phase(&bars.empty[stage], ((n / kStagesB) & 1) ^ 1, ctl));
+                const unsigned stage = n % kStages;
+                ok = __all_sync(kFull, wait_phase(&bars.empty[stage][1], ((n / kStages) & 1) ^ 1, ctl));
                 if (!ok) break;
-                const uint8_t* src = reinterpret_cast<const uint8_t*>(a.a + c * kChunkK + piece * 8);
+                const uint8_t* src = reinterpret_cast<const uint8_t*>(a.a + c * kTileK + piece * 8);
 #pragma unroll
                 for (int j = 0; j < kQuads; ++j)
-                    if (j < quads)
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                                         ((j & 1) ? dst_odd : dst_even) + stage * kBBytes + j * 512),
-                                     "l"(src + static_cast<unsigned long long>(static_cast<unsigned>(row[j])) * row_bytes)
+                    if (j < quads) {
+                        const uint32_t dst = ((j & 1) ? dst_odd : dst_even) + stage * kStageBytes + j * 512;
+                        const uint8_t* from = src + static_cast<unsigned long long>(static_cast<unsigned>(row[j])) * row_bytes;
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(from) : "memory");
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + kChunkBytes), "l"(from + kChunkK * 2)
                                      : "memory");
+                    }
                 asm volatile("cp.async.commit_group;" ::: "memory");
                 if (pending) {
                     asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -268,7 +274,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
                 }
             }
             if (!read) read_rows();
-            n = tile_n + chunks;
+            n = tile_n + KT;
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         if (pending) signal();
@@ -277,8 +283,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
         // One elected thread runs the whole loop: inside its branch the operands stay uniform (174
         // cycles per MMA from a thread picked by its number, 40 from an elected one).
         if (rank == 0 && elect_one()) {
-            // The thread's own instructions set the pace of small steps: one barrier per chunk, looked
-            // at while the chunk before is issued, and addresses that only advance.
+            // The thread's own instructions set the pace of small steps (a wait and a commit cost it about
+            // 250 cycles, an MMA 15; probe): one wait per k-block, looked at while the one before is
+            // issued, and a commit per chunk, so that the first half of a weight slot is free early.
             uint32_t stage = 0, ph = 0, aph = 1;
             int buf = 0;
             bool ok = true;
@@ -290,22 +297,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
                 const uint32_t d = tmem + buf * kRowsMax;
                 ok = wait_phase(&bars.acc_empty[buf], aph, ctl);
                 tc_fence_after();
-                for (int c = 0; c < chunks; ++c) {
+                for (int kb = 0; kb < KT; ++kb) {
                     if (!ready) {
                         ok = wait_phase(&bars.full[stage], ph, ctl);
                         if (!ok) break;
                     }
                     tc_fence_after();
-                    const uint64_t db = smem_desc_advance(desc0, stage * kBBytes);
-                    const uint32_t wa = tmem + kTmemA + (stage % kSlotsA) * (kChunkK / 2);
+                    const uint64_t db = smem_desc_advance(desc0, stage * kStageBytes);
+                    const uint32_t wa = tmem + kTmemA + (stage % kSlotsA) * kChunkK;
 #pragma unroll
-                    for (int k = 0; k < kChunkK / 16; ++k)
-                        mma2_f16_ts(d, wa + k * 8, smem_desc_advance(db, k * 32), idesc, (c | k) ? 1u : 0u);
-                    tc_commit2(&bars.empty[stage]);
-                    stage = (stage + 1) % kStagesB;
+                    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                        for (int k = 0; k < kChunkK / 16; ++k)
+                            mma2_f16_ts(d, wa + h * (kChunkK / 2) + k * 8, smem_desc_advance(db, h * kChunkBytes + k * 32), idesc,
+                                        (kb | h | k) ? 1u : 0u);
+                        tc_commit2(&bars.empty[stage][h]);
+                    }
+                    stage = (stage + 1) % kStages;
                     ph ^= stage == 0;
                     ready = mbar_test_wait(&bars.full[stage], ph);
-                    if (c == 0) {  // the next tile is found while this one is multiplied
+                    if (kb == 0) {  // the next tile is found while this one is multiplied
                         t.next();
                         more = !t.done();
                     }
@@ -321,18 +332,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
         __syncwarp();
     } else if (warp >= kDqWarp0) {
         // ---------------------------------------------------------------- weights
-        const int quarter = warp & 3, par = (warp - kDqWarp0) >> 2;
+        const int quarter = warp & 3, turn = (warp - kDqWarp0) >> 2;
         const int gc = lane >> 2;
         constexpr int kS = SL ? SL : 1;
-        constexpr int kDepth = 2;  // k-blocks of codes in flight
         const int kb_per_group = SL == 1 ? a.g / kTileK : 1;
-        uint4 w[kDepth][4];    // [(rt, h)]
-        uint2 sc[kDepth][kS];  // scales of the columns (rt, h) as fp16
-        uint32_t valid = 0, live = 0;  // bit d: slot d holds a k-block / one inside the weight
-        int f_kb = par;
+        uint4 w[4];    // codes [(rt, h)] of the next k-block of this warp's turn
+        uint2 sc[kS];  // scales of the columns (rt, h) as fp16
+        bool live = false;  // the tile's columns lie in the weight
+        int f_kb = turn;
         const uint8_t* f_at = a.wp;
         const uint8_t* f_scales = a.wp;
-        bool f_live = false;
         auto open_tile = [&]() {  // step over the tiles until f_kb lies in one
             while (!t.done() && f_kb >= KT) {
                 f_kb -= KT;
@@ -340,99 +349,92 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
             }
             if (t.done()) return;
             const int u = (t.ct * 2 + rank) * 4 + quarter;
-            f_live = u < NU;
+            live = u < NU;
             const uint8_t* we = a.wp + static_cast<size_t>(t.e) * a.expert_stride;
             f_at = we + (static_cast<size_t>(u) * KT + f_kb) * kExUnitBytes + lane * 16;
             f_scales = we + a.scale_offset + static_cast<size_t>(u) * (a.K / a.g) * (kExUnitN * 2) + gc * 8;
         };
-        auto fetch = [&](int d) {
-            if (t.done()) {
-                valid &= ~(1u << d);
-                return;
-            }
-            valid |= 1u << d;
-            live = f_live ? live | (1u << d) : live & ~(1u << d);
-            if (f_live) {
+        bool valid = false, w_live = false;  // w holds a k-block / one inside the weight
+        auto fetch = [&]() {
+            valid = !t.done();
+            w_live = live;
+            if (!valid) return;
+            if (live) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[d][i] = ldg_stream16(f_at + i * 512);
-                f_at += 2 * kExUnitBytes;
+                for (int i = 0; i < 4; ++i) w[i] = ldg_stream16(f_at + i * 512);
+                f_at += kDqTurns * kExUnitBytes;
                 if (SL) {
 #pragma unroll
                     for (int i = 0; i < kS; ++i) {
                         const int grp = SL == 1 ? (kb_per_group == 1 ? f_kb : f_kb / kb_per_group) : f_kb * SL + i;
-                        sc[d][i] = __ldg(reinterpret_cast<const uint2*>(f_scales + static_cast<size_t>(grp) * (kExUnitN * 2)));
+                        sc[i] = __ldg(reinterpret_cast<const uint2*>(f_scales + static_cast<size_t>(grp) * (kExUnitN * 2)));
                     }
                 }
             }
-            f_kb += 2;
+            f_kb += kDqTurns;
             if (f_kb >= KT) open_tile();
         };
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < kS; ++i) sc[i] = make_uint2(0, 0);
         open_tile();
-#pragma unroll
-        for (int d = 0; d < kDepth; ++d) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[d][i] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int i = 0; i < kS; ++i) sc[d][i] = make_uint2(0, 0);
-            fetch(d);
-        }
+        fetch();
         const uint32_t tbase = tmem + kTmemA + (static_cast<uint32_t>(quarter * 32) << 16);
-        unsigned n = 2 * par;  // chunk number of the k-block's first half
+        unsigned n = turn;  // k-block
         bool ok = true;
-        while (ok && (valid & 1u)) {
+        while (ok && valid) {
+            const bool stored = w_live;
+            uint32_t v[2][2][16];  // [half][rt]: converted before the slot is waited for
 #pragma unroll
-            for (int d = 0; d < kDepth; ++d) {
-                if (!ok || !((valid >> d) & 1u)) break;
-                uint32_t v[2][2][16];  // [half of the k-block][rt]
+            for (int half = 0; half < 2; ++half)
 #pragma unroll
-                for (int half = 0; half < 2; ++half)
+                for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
-                    for (int rt = 0; rt < 2; ++rt)
+                    for (int b = 0; b < 2; ++b)
 #pragma unroll
-                        for (int b = 0; b < 2; ++b)
+                        for (int h = 0; h < 2; ++h) {
+                            const uint4 q4 = w[rt * 2 + h];
+                            uint32_t p[4];
+                            dequant8(half ? (b ? q4.w : q4.z) : (b ? q4.y : q4.x), p);
+                            if (SL) {
+                                const uint2 sv = sc[SL == 4 ? (2 * half + b) % kS : SL == 2 ? half % kS : 0];
+                                const uint32_t pair = rt ? sv.y : sv.x;
+                                const __half2 s2 = *reinterpret_cast<const __half2*>(&pair);
+                                const __half2 sb = h ? __high2half2(s2) : __low2half2(s2);
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const uint4 q4 = w[d][rt * 2 + h];
-                                uint32_t p[4];
-                                dequant8(half ? (b ? q4.w : q4.z) : (b ? q4.y : q4.x), p);
-                                if (SL) {
-                                    const uint2 sv = sc[d][SL == 4 ? (2 * half + b) % kS : SL == 2 ? half % kS : 0];
-                                    const uint32_t pair = rt ? sv.y : sv.x;
-                                    const __half2 s2 = *reinterpret_cast<const __half2*>(&pair);
-                                    const __half2 sb = h ? __high2half2(s2) : __low2half2(s2);
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) {
-                                        const __half2 m = __hmul2(*reinterpret_cast<__half2*>(&p[i]), sb);
-                                        p[i] = *reinterpret_cast<const uint32_t*>(&m);
-                                    }
+                                for (int i = 0; i < 4; ++i) {
+                                    const __half2 m = __hmul2(*reinterpret_cast<__half2*>(&p[i]), sb);
+                                    p[i] = *reinterpret_cast<const uint32_t*>(&m);
                                 }
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) v[half][rt][2 * (4 * b + i) + h] = p[i];
                             }
-                const bool stored = (live >> d) & 1u;
-                fetch(d);
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const unsigned c = n + half;
-                    // the chunk four before has left the slot; the first four find it empty
-                    if (c >= kSlotsA) {
-                        const unsigned before = c - kSlotsA;
-                        ok = __all_sync(kFull, wait_phase(&bars.empty[before % kStagesB], (before / kStagesB) & 1, ctl));
-                        if (!ok) break;
-                        tc_fence_after();
-                    }
-                    if (stored) {
-                        const uint32_t slot = tbase + (c % kSlotsA) * (kChunkK / 2);
-                        tmem_st_16x128b_x8(slot, v[half][0]);
-                        tmem_st_16x128b_x8(slot + (16u << 16), v[half][1]);
-                        tmem_st_wait();
-                        tc_fence_before();
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_leader(&bars.full[c % kStagesB]);
+                            for (int i = 0; i < 4; ++i) v[half][rt][2 * (4 * b + i) + h] = p[i];
+                        }
+            fetch();
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                // the k-block two before has left this half of the slot; the first two find it empty
+                if (n >= kSlotsA) {
+                    const unsigned before = n - kSlotsA;
+                    ok = __all_sync(kFull, wait_phase(&bars.empty[before % kStages][half], (before / kStages) & 1, ctl));
+                    if (!ok) break;
+                    tc_fence_after();
                 }
-                n += 4;
+                if (stored) {
+                    const uint32_t slot = tbase + (n % kSlotsA) * kChunkK + half * (kChunkK / 2);
+                    tmem_st_16x128b_x8(slot, v[half][0]);
+                    tmem_st_16x128b_x8(slot + (16u << 16), v[half][1]);
+                }
             }
+            if (!ok) break;
+            if (stored) {
+                tmem_st_wait();
+                tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive_leader(&bars.full[n % kStages]);
+            n += kDqTurns;
         }
     } else {
         // ---------------------------------------------------------------- epilogue
