@@ -623,16 +623,18 @@ cudaError_t configure_expert_kernels() {
 }
 
 // Rows per expert, were the pairs spread evenly, up to which mma.sync tiles of 8 rows beat the tcgen05
-// tiles, which need the same time up to some hundred rows. Measured at 8 / 12 / 16 rows: 64 experts of
-// 2048 x 2048 48.5 / 60.1 / 74.6 us against 58.6 / 58.7 / 59.0, 8 of 4096 x 8192 51.3 / 60.6 / 70.9
-// against 64.4 / 64.3 / 64.2.
-constexpr int kFewRows = 12;
+// tiles, whose time is that of the dequantised weight and of each group's sums up to some hundred rows.
+// Measured (tiles of 8 rows against tcgen05 tiles): g = 128, 64 experts of 2048 x 2048: 12 rows 60.0 us
+// against 65.1, 16 rows 74.9 / 65.4; 8 of 4096 x 8192: 61.6 / 71.4, 70.8 / 70.9; g = K, 32 of 2048 x
+// 2048: 12 rows 34.7 / 36.2, 16 rows 39.7 / 36.3. g = 64, 128 of 1024 x 1536: 20 rows 74.1 / 81.2, 24
+// rows 83.8 / 82.1. g = 32, 32 of 2048 x 2048: 32 rows 70.3 / 97.8, 96 rows 180 / 137.
+int few_rows(const ExpertArgs& a) { return a.g == 32 ? 48 : a.g == 64 ? 22 : 14; }
 
 cudaError_t launch_experts(const ExpertArgs& a, const DeviceInfo& d, cudaStream_t st) {
     const long long per_expert = (static_cast<long long>(a.pairs) + a.E - 1) / a.E;
     if (experts_token_form(a.pairs, a.E)) return launch_token<false>(a, nullptr, nullptr, 1, d.num_sms, st);
     // rows of 16 warps' places reach further than those of 24: K up to 11008 against 9728
-    if (per_expert > kFewRows || Small<0, 16>::places(a.K) == 0) return launch_experts_large(a, d, st);
+    if (per_expert > few_rows(a) || Small<0, 16>::places(a.K) == 0) return launch_experts_large(a, d, st);
     if (Small<0, 24>::places(a.K)) return launch_w<24>(a, d.num_sms, st);
     return launch_w<16>(a, d.num_sms, st);
 }

@@ -1,23 +1,25 @@
 // The experts' 4-bit products for many rows per expert: tcgen05 tiles over the lists.
 //
-// Tile: 128 columns of one expert's weight (the MMA's M) x up to 192 of its rows (the MMA's N),
-// all of K in chunks of 64 rows. One persistent CTA per SM, warp-specialised:
-//   warps 0..2   gather the rows' 128-byte pieces with cp.async into a ring of 16 chunks, each
-//                warp every third chunk;
-//   warp 3       one elected thread issues the MMAs: weights from tensor memory, rows from shared
-//                memory (128-byte swizzle), fp32 sums in tensor memory, two accumulators of 192
-//                columns used in turn;
-//   warps 4..7   epilogue of the tile before, while the next one is multiplied;
-//   warps 8..15  dequantise: warp 8 + w takes the tile's columns 32 (w % 4) .. + 31 of every second
-//                k-block, loads its codes straight from global memory several k-blocks ahead
-//                (across tiles) and stores fp16 weights (q - 8) * s, rounded once, into one of
-//                four 64-row slots in tensor memory.
+// Tile: 256 columns of one expert's weight (the MMA's M, 128 for each CTA of a pair) x up to 128 of its
+// rows (the MMA's N), all of K in k-blocks of 128 rows. One persistent CTA per SM, warp-specialised:
+//   warps 0..2    gather the rows' 128-byte pieces with cp.async into a ring of 8 k-blocks, each warp
+//                 every third k-block;
+//   warp 3        one elected thread issues the pair's MMAs: weights from tensor memory, rows from
+//                 shared memory (128-byte swizzle), the sums of one scale group to tensor memory;
+//   warps 4..19   add the groups' sums up: warp 4 + w takes columns 32 (w % 4) .. + 31 and every fourth
+//                 16 rows, reads a group's sums while the next group is multiplied, and adds scale
+//                 times sum in its registers, fp32; at the tile's end it stores its rows;
+//   warps 20..27  dequantise: warp 20 + w takes columns 32 (w % 4) .. + 31 of every second k-block,
+//                 loads its codes straight from global memory a turn ahead (across tiles) and
+//                 stores exact fp16 q - 8 into one of four slots in tensor memory.
 // An expert's rows are split evenly over its row tiles. Tiles of the same rows are neighbours, so
 // that the rows are gathered from L2 after the first time.
-// Why so: the weight operand in tensor memory saves the ~32 cycles that each MMA spends on loading
-// it from shared memory (probe, 128 x 256 x 16: 137 cycles against 168), and 192 rows leave tensor
-// memory for a second accumulator. TMA gather4 in place of cp.async moves a row of 128 bytes per 14
-// cycles and set the pace at a quarter of this kernel's rate.
+// Why so: the weights stay exact. With (q - 8) * s rounded to fp16 in the dequantisation the outputs
+// were 1.6 times as far from the exact product as the fp16 rounding of the output alone. The weight
+// operand in tensor memory saves the ~32 cycles that each MMA spends on loading it from shared memory
+// (probe, 128 x 256 x 16: 137 cycles against 168). TMA gather4 in place of cp.async moves a row of 128
+// bytes per 14 cycles and set the pace at a quarter of this kernel's rate. The pair halves the rows'
+// way from L2, which one CTA alone loaded to two thirds.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
@@ -30,27 +32,25 @@ namespace wq {
 
 namespace {
 
-constexpr int kDqTurns = 2;                        // a k-block in so many belongs to a dequant warp
-constexpr int kLThreads = (8 + 4 * kDqTurns) * 32;
-constexpr int kRowsMax = 192;                      // rows of a tile
-constexpr int kColsL = 128;                        // columns of a tile
-constexpr int kChunkK = 64;                        // weight rows of a stage: one 128-byte swizzle span
+constexpr int kLThreads = 28 * 32;
+constexpr int kRowsMax = 128;                      // rows of a tile
+constexpr int kColsL = 128;                        // columns of a tile per CTA
+constexpr int kChunkK = 64;                        // weight rows of a chunk: one 128-byte swizzle span
 constexpr int kHalfRows = kRowsMax / 2;            // rows of a tile that one CTA of the pair holds
-constexpr int kChunkBytes = kHalfRows * kChunkK * 2;  // 12 KiB
+constexpr int kChunkBytes = kHalfRows * kChunkK * 2;  // 8 KiB
 constexpr int kStageBytes = 2 * kChunkBytes;       // a k-block: two chunks
 constexpr int kStages = 8;                         // k-blocks of rows in shared memory
-constexpr int kSlotsA = 2;                         // k-blocks of weights in tensor memory
-constexpr int kTmemA = 2 * kRowsMax;               // tensor-memory column of the weight slots
+constexpr int kSlotsA = 4;                         // k-blocks of weights in tensor memory
+constexpr int kTmemA = 2 * kRowsMax;               // their first column, behind two groups' sums
 constexpr int kSmemL = kStages * kStageBytes + 1024;  // + alignment of the first stage
-constexpr int kGatherWarps = 3, kMmaWarp = 3, kEpiWarp0 = 4, kDqWarp0 = 8;
+constexpr int kGatherWarps = 3, kMmaWarp = 3, kAddWarp0 = 4, kAddWarps = 16, kDqWarp0 = 20, kDqTurns = 2;
 constexpr int kQuads = kHalfRows / 4;              // a warp's copy instruction takes four rows
-
 constexpr int kYRow = 80, kYRowGated = 48;         // bytes of an output row on its way out, with padding
-constexpr int kYBytes = 32 * kYRow;
+constexpr int kYBytes = 16 * kYRow;
 
 struct Bars {
-    uint64_t full[kStages], empty[kStages][2];  // empty: per chunk
-    uint64_t acc_full[2], acc_empty[2], drain;
+    uint64_t full[kStages], empty[kStages];
+    uint64_t sum_full[2], sum_empty[2], drain;
 };
 
 struct LargeArgs {
@@ -144,26 +144,23 @@ __device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&v)[32]) {
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&v)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
-          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
-          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
         : "r"(taddr)
         : "memory");
 }
 
-// SL as in the small kernel: scales per k-block and column; 0: per-column, applied in the epilogue.
+// SL as in the small kernel: scales per k-block and column; 0: per-column.
 template <int SL>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) experts_large_kernel(LargeArgs args) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ Bars bars;
     __shared__ int s_start[kExMaxExperts + 1], s_tiles[kExMaxExperts + 1], s_each[kExMaxExperts], s_scratch[kLThreads / 32];
-    __shared__ __align__(16) uint8_t stage_y[4 * kYBytes];
+    __shared__ __align__(16) uint8_t stage_y[kAddWarps * kYBytes];
     __shared__ uint32_t s_tmem;
     __shared__ int s_stop;
     const ExpertArgs& a = args.e;
@@ -174,12 +171,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&bars.full[i], 2 + 8);  // a gather warp and four dequant warps of each CTA
-            mbar_init(&bars.empty[i][0], 1);
-            mbar_init(&bars.empty[i][1], 1);
+            mbar_init(&bars.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars.acc_full[i], 1);
-            mbar_init(&bars.acc_empty[i], 8);
+            mbar_init(&bars.sum_full[i], 1);
+            mbar_init(&bars.sum_empty[i], 2 * kAddWarps);
         }
         mbar_init(&bars.drain, 1);
         s_stop = 0;
@@ -195,6 +191,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
     const uint32_t tmem = s_tmem;
     const Ctl ctl{&s_stop, a.status, args.timeout_ns};
     const int KT = a.K / kTileK;
+    const int kb_per_group = SL == 0 ? KT : SL == 1 ? a.g / kTileK : 1;  // k-blocks summed in tensor memory
     const int CT = (a.N + 2 * kColsL - 1) / (2 * kColsL), NU = ex_units(a.N);
     // column tiles of the same rows are neighbours; pair b takes tiles b, b + pairs, ...
     Walk t(CT, a.E, blockIdx.x / 2, gridDim.x / 2, s_start, s_tiles, s_each);
@@ -249,7 +246,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
             for (int c = (warp + kGatherWarps - tile_n % kGatherWarps) % kGatherWarps; c < KT; c += kGatherWarps) {
                 n = tile_n + c;
                 const unsigned stage = n % kStages;
-                ok = __all_sync(kFull, wait_phase(&bars.empty[stage][1], ((n / kStages) & 1) ^ 1, ctl));
+                ok = __all_sync(kFull, wait_phase(&bars.empty[stage], ((n / kStages) & 1) ^ 1, ctl));
                 if (!ok) break;
                 const uint8_t* src = reinterpret_cast<const uint8_t*>(a.a + c * kTileK + piece * 8);
 #pragma unroll
@@ -284,34 +281,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
         // cycles per MMA from a thread picked by its number, 40 from an elected one).
         if (rank == 0 && elect_one()) {
             // The thread's own instructions set the pace of small steps (a wait and a commit cost it about
-            // 250 cycles, an MMA 15; probe): one wait per k-block, looked at while the one before is
-            // issued, and a commit per chunk, so that the first half of a weight slot is free early.
-            uint32_t stage = 0, ph = 0, aph = 1;
-            int buf = 0;
+            // 250 cycles, an MMA 15; probe): a wait per k-block, looked at while the one before is issued.
+            uint32_t stage = 0, ph = 0;
+            unsigned m = 0;  // groups so far: sums m & 1
             bool ok = true;
             const uint64_t desc0 = smem_desc_sw128(smem_addr(ring));
             bool more = !t.done();
             bool ready = mbar_test_wait(&bars.full[0], 0);
             while (ok && more) {
                 const uint32_t idesc = idesc_f16_f32(2 * kColsL, (t.nrows + 15) / 16 * 16);
-                const uint32_t d = tmem + buf * kRowsMax;
-                ok = wait_phase(&bars.acc_empty[buf], aph, ctl);
-                tc_fence_after();
+                int in_group = 0;  // k-blocks of the group that have been issued
                 for (int kb = 0; kb < KT; ++kb) {
-                    if (!ready) {
-                        ok = wait_phase(&bars.full[stage], ph, ctl);
-                        if (!ok) break;
-                    }
+                    if (SL < 2 && in_group == 0) ok = wait_phase(&bars.sum_empty[m & 1], ((m >> 1) & 1) ^ 1, ctl);
+                    if (ok && !ready) ok = wait_phase(&bars.full[stage], ph, ctl);
+                    if (!ok) break;
                     tc_fence_after();
                     const uint64_t db = smem_desc_advance(desc0, stage * kStageBytes);
                     const uint32_t wa = tmem + kTmemA + (stage % kSlotsA) * kChunkK;
+                    constexpr int kGroups = SL < 2 ? 1 : SL;  // groups of a k-block
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
+                    for (int q = 0; q < kGroups; ++q) {
+                        if (SL >= 2) {
+                            ok = wait_phase(&bars.sum_empty[m & 1], ((m >> 1) & 1) ^ 1, ctl);
+                            if (!ok) break;
+                            tc_fence_after();
+                        }
+                        const uint32_t d = tmem + (m & 1) * kRowsMax;
 #pragma unroll
-                        for (int k = 0; k < kChunkK / 16; ++k)
-                            mma2_f16_ts(d, wa + h * (kChunkK / 2) + k * 8, smem_desc_advance(db, h * kChunkBytes + k * 32), idesc,
-                                        (kb | h | k) ? 1u : 0u);
-                        tc_commit2(&bars.empty[stage][h]);
+                        for (int k = q * (8 / kGroups); k < (q + 1) * (8 / kGroups); ++k)
+                            mma2_f16_ts(d, wa + k * 8, smem_desc_advance(db, (k >> 2) * kChunkBytes + (k & 3) * 32), idesc,
+                                        (k > q * (8 / kGroups) || in_group > 0) ? 1u : 0u);
+                        if (SL >= 2) {
+                            tc_commit2(&bars.sum_full[m & 1]);
+                            ++m;
+                        }
+                    }
+                    if (!ok) break;
+                    tc_commit2(&bars.empty[stage]);
+                    if (SL < 2 && ++in_group == kb_per_group) {
+                        tc_commit2(&bars.sum_full[m & 1]);
+                        ++m;
+                        in_group = 0;
                     }
                     stage = (stage + 1) % kStages;
                     ph ^= stage == 0;
@@ -321,9 +331,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
                         more = !t.done();
                     }
                 }
-                if (ok) tc_commit2(&bars.acc_full[buf]);
-                buf ^= 1;
-                if (buf == 0) aph ^= 1;
             }
             // every MMA done before the CTA frees its tensor memory
             tc_commit2(&bars.drain);
@@ -333,15 +340,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
     } else if (warp >= kDqWarp0) {
         // ---------------------------------------------------------------- weights
         const int quarter = warp & 3, turn = (warp - kDqWarp0) >> 2;
-        const int gc = lane >> 2;
-        constexpr int kS = SL ? SL : 1;
-        const int kb_per_group = SL == 1 ? a.g / kTileK : 1;
-        uint4 w[4];    // codes [(rt, h)] of the next k-block of this warp's turn
-        uint2 sc[kS];  // scales of the columns (rt, h) as fp16
-        bool live = false;  // the tile's columns lie in the weight
+        constexpr int kDepth = 1;  // k-blocks of codes in flight
+        uint4 w[kDepth][4];        // codes [(rt, h)]
+        uint32_t valid = 0, inside = 0;  // bit d: slot d holds a k-block / one inside the weight
+        bool live = false;
         int f_kb = turn;
         const uint8_t* f_at = a.wp;
-        const uint8_t* f_scales = a.wp;
         auto open_tile = [&]() {  // step over the tiles until f_kb lies in one
             while (!t.done() && f_kb >= KT) {
                 f_kb -= KT;
@@ -350,163 +354,166 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
             if (t.done()) return;
             const int u = (t.ct * 2 + rank) * 4 + quarter;
             live = u < NU;
-            const uint8_t* we = a.wp + static_cast<size_t>(t.e) * a.expert_stride;
-            f_at = we + (static_cast<size_t>(u) * KT + f_kb) * kExUnitBytes + lane * 16;
-            f_scales = we + a.scale_offset + static_cast<size_t>(u) * (a.K / a.g) * (kExUnitN * 2) + gc * 8;
+            f_at = a.wp + static_cast<size_t>(t.e) * a.expert_stride + (static_cast<size_t>(u) * KT + f_kb) * kExUnitBytes +
+                   lane * 16;
         };
-        bool valid = false, w_live = false;  // w holds a k-block / one inside the weight
-        auto fetch = [&]() {
-            valid = !t.done();
-            w_live = live;
-            if (!valid) return;
+        auto fetch = [&](int d) {
+            valid &= ~(1u << d);
+            if (t.done()) return;
+            valid |= 1u << d;
+            inside = live ? inside | (1u << d) : inside & ~(1u << d);
             if (live) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = ldg_stream16(f_at + i * 512);
+                for (int i = 0; i < 4; ++i) w[d][i] = ldg_stream16(f_at + i * 512);
                 f_at += kDqTurns * kExUnitBytes;
-                if (SL) {
-#pragma unroll
-                    for (int i = 0; i < kS; ++i) {
-                        const int grp = SL == 1 ? (kb_per_group == 1 ? f_kb : f_kb / kb_per_group) : f_kb * SL + i;
-                        sc[i] = __ldg(reinterpret_cast<const uint2*>(f_scales + static_cast<size_t>(grp) * (kExUnitN * 2)));
-                    }
-                }
             }
             f_kb += kDqTurns;
             if (f_kb >= KT) open_tile();
         };
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < kS; ++i) sc[i] = make_uint2(0, 0);
         open_tile();
-        fetch();
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[d][i] = make_uint4(0, 0, 0, 0);
+            fetch(d);
+        }
         const uint32_t tbase = tmem + kTmemA + (static_cast<uint32_t>(quarter * 32) << 16);
         unsigned n = turn;  // k-block
         bool ok = true;
-        while (ok && valid) {
-            const bool stored = w_live;
-            uint32_t v[2][2][16];  // [half][rt]: converted before the slot is waited for
+        while (ok && (valid & 1u)) {
 #pragma unroll
-            for (int half = 0; half < 2; ++half)
+            for (int d = 0; d < kDepth; ++d) {
+                if (!ok || !((valid >> d) & 1u)) break;
+                const bool store = (inside >> d) & 1u;
+                const uint32_t slot = tbase + (n % kSlotsA) * kChunkK;
 #pragma unroll
-                for (int rt = 0; rt < 2; ++rt)
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t v[2][16];
 #pragma unroll
-                    for (int b = 0; b < 2; ++b)
+                    for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint4 q4 = w[rt * 2 + h];
-                            uint32_t p[4];
-                            dequant8(half ? (b ? q4.w : q4.z) : (b ? q4.y : q4.x), p);
-                            if (SL) {
-                                const uint2 sv = sc[SL == 4 ? (2 * half + b) % kS : SL == 2 ? half % kS : 0];
-                                const uint32_t pair = rt ? sv.y : sv.x;
-                                const __half2 s2 = *reinterpret_cast<const __half2*>(&pair);
-                                const __half2 sb = h ? __high2half2(s2) : __low2half2(s2);
+                        for (int b = 0; b < 2; ++b)
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const __half2 m = __hmul2(*reinterpret_cast<__half2*>(&p[i]), sb);
-                                    p[i] = *reinterpret_cast<const uint32_t*>(&m);
-                                }
+                            for (int h = 0; h < 2; ++h) {
+                                const uint4 q4 = w[d][rt * 2 + h];
+                                uint32_t p[4];
+                                dequant8(half ? (b ? q4.w : q4.z) : (b ? q4.y : q4.x), p);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) v[rt][2 * (4 * b + i) + h] = p[i];
                             }
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) v[half][rt][2 * (4 * b + i) + h] = p[i];
-                        }
-            fetch();
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                // the k-block two before has left this half of the slot; the first two find it empty
-                if (n >= kSlotsA) {
-                    const unsigned before = n - kSlotsA;
-                    ok = __all_sync(kFull, wait_phase(&bars.empty[before % kStages][half], (before / kStages) & 1, ctl));
-                    if (!ok) break;
-                    tc_fence_after();
+                    if (half == 1) fetch(d);
+                    // the k-block four before has left the slot; the first four find it empty
+                    if (half == 0 && n >= kSlotsA) {
+                        const unsigned before = n - kSlotsA;
+                        ok = __all_sync(kFull, wait_phase(&bars.empty[before % kStages], (before / kStages) & 1, ctl));
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+                    if (store) {
+                        tmem_st_16x128b_x8(slot + half * (kChunkK / 2), v[0]);
+                        tmem_st_16x128b_x8(slot + half * (kChunkK / 2) + (16u << 16), v[1]);
+                    }
                 }
-                if (stored) {
-                    const uint32_t slot = tbase + (n % kSlotsA) * kChunkK + half * (kChunkK / 2);
-                    tmem_st_16x128b_x8(slot, v[half][0]);
-                    tmem_st_16x128b_x8(slot + (16u << 16), v[half][1]);
+                if (!ok) break;
+                if (store) {
+                    tmem_st_wait();
+                    tc_fence_before();
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive_leader(&bars.full[n % kStages]);
+                n += kDqTurns;
             }
-            if (!ok) break;
-            if (stored) {
-                tmem_st_wait();
-                tc_fence_before();
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive_leader(&bars.full[n % kStages]);
-            n += kDqTurns;
         }
     } else {
-        // ---------------------------------------------------------------- epilogue
-        const int quarter = warp & 3;
+        // ---------------------------------------------------------------- the groups' sums, the output
+        const int quarter = warp & 3, part = (warp - kAddWarp0) >> 2;  // 16-row pieces 4i + part
         const int n_out = a.gated ? a.N / 2 : a.N;
-        int buf = 0;
-        uint32_t ph = 0;
-        for (; !t.done(); t.next()) {
+        const int groups = SL == 0 ? 1 : a.K / a.g;
+        const uint32_t tbase = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        uint8_t* out = stage_y + (warp - kAddWarp0) * kYBytes;
+        unsigned m = 0;  // groups so far
+        bool ok = true;
+        for (; ok && !t.done(); t.next()) {
             const int ct = t.ct * 2 + rank;
-            const int v = ct * kColsL + quarter * 32 + lane;  // layout column of this lane
-            float cs = 1.f;
-            if (SL == 0 && v < a.N) {
-                const __half* sp = reinterpret_cast<const __half*>(a.wp + static_cast<size_t>(t.e) * a.expert_stride +
-                                                                   a.scale_offset) + static_cast<size_t>(v / 32) * kExUnitN;
-                cs = __half2float(sp[(v & 7) * 4 + ((v >> 4) & 1) * 2 + ((v >> 3) & 1)]);
+            const int u = ct * 4 + quarter;  // this warp's 32 columns
+            const bool live = u < NU;
+            const int pieces = (t.nrows + 15) / 16;
+            const __half* sp = reinterpret_cast<const __half*>(a.wp + static_cast<size_t>(t.e) * a.expert_stride +
+                                                               a.scale_offset) +
+                               static_cast<size_t>(live ? u : 0) * groups * kExUnitN +
+                               (lane & 7) * 4 + (lane >> 4) * 2 + ((lane >> 3) & 1);
+            // lane l % 16 keeps the pair of that row of each piece
+            int pair[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = (4 * i + part) * 16 + (lane & 15);
+                pair[i] = r < t.nrows ? __ldg(a.rows + t.row0 + r) : -1;
             }
-            // lane l of each 32 rows keeps row l's pair; the next 32 are read while these are stored
-            int pair_next = lane < t.nrows ? __ldg(a.rows + t.row0 + lane) : -1;
-            if (!__all_sync(kFull, wait_phase(&bars.acc_full[buf], ph, ctl))) break;
-            tc_fence_after();
-            const uint32_t taddr = tmem + buf * kRowsMax + (static_cast<uint32_t>(quarter * 32) << 16);
-            uint8_t* out = stage_y + quarter * kYBytes;
-            for (int m0 = 0; m0 < t.nrows; m0 += 32) {
-                uint32_t d[32];
-                tmem_ld_x32(taddr + m0, d);
-                const int pair = static_cast<unsigned>(pair_next) < static_cast<unsigned>(a.pairs) ? pair_next : -1;
-                pair_next = m0 + 32 + lane < t.nrows ? __ldg(a.rows + t.row0 + m0 + 32 + lane) : -1;
-                tmem_ld_wait();
-                // 32 rows x this warp's columns turned round in shared memory: rows of 64 (gated: 32)
-                // bytes, so that a row leaves in 16-byte stores
+            float acc[2][16];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[i][r] = 0.f;
+            __half next = __ldg(sp);
+            for (int g = 0; g < groups; ++g, ++m) {
+                const float scale = __half2float(next);
+                sp += kExUnitN;
+                if (g + 1 < groups) next = __ldg(sp);
+                ok = __all_sync(kFull, wait_phase(&bars.sum_full[m & 1], (m >> 1) & 1, ctl));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t from = tbase + (m & 1) * kRowsMax;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (4 * i + part < pieces) {
+                        uint32_t d[16];
+                        tmem_ld_x16(from + (4 * i + part) * 16, d);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) acc[i][r] += scale * __uint_as_float(d[r]);
+                    }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_leader(&bars.sum_empty[m & 1]);
+            }
+            if (!ok) break;
+            // 16 rows x 32 columns at a time turned round in shared memory: rows of 64 (gated: 32)
+            // bytes, so that a row leaves in 16-byte stores
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (4 * i + part >= pieces) continue;
+                const int p_row = static_cast<unsigned>(pair[i]) < static_cast<unsigned>(a.pairs) ? pair[i] : -1;
                 __syncwarp();
                 if (a.gated) {
-                    // gate lanes take the first 16 rows, up lanes the others
+                    // gate lanes take the first 8 rows, up lanes the others
                     const bool up = lane & 8;
-                    uint16_t* col = reinterpret_cast<uint16_t*>(out) + ((lane >> 4) * 8 + (lane & 7)) + (up ? 16 * (kYRowGated / 2) : 0);
+                    uint16_t* col = reinterpret_cast<uint16_t*>(out) + ((lane >> 4) * 8 + (lane & 7)) + (up ? 8 * (kYRowGated / 2) : 0);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float x0 = __uint_as_float(d[i]) * cs, x1 = __uint_as_float(d[i + 16]) * cs;
-                        const float other = __shfl_xor_sync(kFull, up ? x0 : x1, 8);
-                        const float h = up ? silu_mul(other, x1) : silu_mul(x0, other);
-                        col[i * (kYRowGated / 2)] = __half_as_ushort(__float2half_rn(h));
+                    for (int r = 0; r < 8; ++r) {
+                        const float other = __shfl_xor_sync(kFull, up ? acc[i][r] : acc[i][r + 8], 8);
+                        const float h = up ? silu_mul(other, acc[i][r + 8]) : silu_mul(acc[i][r], other);
+                        col[r * (kYRowGated / 2)] = __half_as_ushort(__float2half_rn(h));
                     }
                     __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int m = i * 16 + (lane >> 1);
-                        const int p = __shfl_sync(kFull, pair, m);
-                        const int n = ct * (kColsL / 2) + quarter * 16 + (lane & 1) * 8;
-                        const uint4 v4 = *reinterpret_cast<const uint4*>(out + m * kYRowGated + (lane & 1) * 16);
-                        if (p >= 0 && n < n_out) *reinterpret_cast<uint4*>(a.y + static_cast<size_t>(p) * n_out + n) = v4;
-                    }
+                    const int p = __shfl_sync(kFull, p_row, lane >> 1);
+                    const int n = ct * (kColsL / 2) + quarter * 16 + (lane & 1) * 8;
+                    const uint4 v4 = *reinterpret_cast<const uint4*>(out + (lane >> 1) * kYRowGated + (lane & 1) * 16);
+                    if (p >= 0 && n < n_out) *reinterpret_cast<uint4*>(a.y + static_cast<size_t>(p) * n_out + n) = v4;
                 } else {
                     uint16_t* col = reinterpret_cast<uint16_t*>(out) + lane;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        col[i * (kYRow / 2)] = __half_as_ushort(__float2half_rn(__uint_as_float(d[i]) * cs));
+                    for (int r = 0; r < 16; ++r) col[r * (kYRow / 2)] = __half_as_ushort(__float2half_rn(acc[i][r]));
                     __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int m = i * 8 + (lane >> 2);
-                        const int p = __shfl_sync(kFull, pair, m);
+                    for (int k = 0; k < 2; ++k) {
+                        const int row = k * 8 + (lane >> 2);
+                        const int p = __shfl_sync(kFull, p_row, row);
                         const int n = ct * kColsL + quarter * 32 + (lane & 3) * 8;
-                        const uint4 v4 = *reinterpret_cast<const uint4*>(out + m * kYRow + (lane & 3) * 16);
+                        const uint4 v4 = *reinterpret_cast<const uint4*>(out + row * kYRow + (lane & 3) * 16);
                         if (p >= 0 && n < n_out) *reinterpret_cast<uint4*>(a.y + static_cast<size_t>(p) * n_out + n) = v4;
                     }
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_leader(&bars.acc_empty[buf]);
-            buf ^= 1;
-            if (buf == 0) ph ^= 1;
         }
     }
     tc_fence_before();

@@ -316,7 +316,7 @@ WQ_API int wq_gemm_w4a16_noalloc(const uint16_t* A, const void* Wp, uint16_t* Y,
  *   gated 0: Y[p, n] = A[p / top_k] . W_e[:, n]                        Y fp16 [T * top_k, N]
  *   gated 1: Y[p, i] = silu(gate) * up, gate = A[p / top_k] . W_e[:, i],
  *            up = A[p / top_k] . W_e[:, I + i]                         Y fp16 [T * top_k, I]
- * A fp16 [T, K]; products of exact (q - 8) or of weights rounded once to fp16, fp32 sums, Y
+ * A fp16 [T, K]; products of exact (q - 8), each group's fp32 sum times its scale, fp32 sums, Y
  * rounded once. Rows of Y of pairs that are in no list are left as they were. The lists are read
  * on the device: an entry of rows outside [0, T * top_k) is skipped and records
  * WQ_ERR_INVALID_ARG in the device status word (wq_get_device_status), offsets are taken as if

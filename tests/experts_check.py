@@ -3,8 +3,7 @@
 Bounds, derived before any run. A product sums K exact products of fp16 values in K/16 matrix
 instructions and at most 16 further fp32 additions, each off by at most 2^-22 of the sum of
 magnitudes S = sum |a w| (the instruction may truncate its 16 + 1 addends):
-    sum:   |d - d*| <= (K/16 + 16) 2^-22 S  (+ 2^-11 S where weights are rounded once to fp16:
-           half a step of fp16 relative to the value), plus 2^-23 |d| for the fp32 scale product
+    sum:   |d - d*| <= (K/16 + 16) 2^-22 S, plus 2^-23 |d| for the fp32 scale product
     fp16:  half a step, 2^-11 |y|, or 2^-25 where y is below the normal range.
 Gated: silu' lies in [-0.1, 1.1], so the errors of the sums enter as 1.1 |up| eg + |silu| eu,
 and fp32 exp, division and products add less than 2^-18 |h| (exp's error grows with |gate| <= 40).
@@ -23,17 +22,17 @@ def half_step(y):
     return np.maximum(2.0 ** -11 * np.abs(y), 2.0 ** -25)
 
 
-def sum_bound(y, absdot, K, rounded_weights):
-    return ((K / 16 + 16) * 2.0 ** -22 + (2.0 ** -11 if rounded_weights else 0.0)) * absdot + 2.0 ** -23 * np.abs(y)
+def sum_bound(y, absdot, K):
+    return (K / 16 + 16) * 2.0 ** -22 * absdot + 2.0 ** -23 * np.abs(y)
 
 
-def product_bound(y, absdot, K, rounded_weights=False):
-    e = sum_bound(y, absdot, K, rounded_weights)
+def product_bound(y, absdot, K):
+    e = sum_bound(y, absdot, K)
     return e + half_step(np.abs(y) + e)
 
 
-def gated_bound(y, absdot, K, rounded_weights=False):
-    e = sum_bound(y, absdot, K, rounded_weights)
+def gated_bound(y, absdot, K):
+    e = sum_bound(y, absdot, K)
     half = y.shape[1] // 2
     gate, up = y[:, :half], y[:, half:]
     silu = gate / (1.0 + np.exp(-gate))
@@ -43,9 +42,9 @@ def gated_bound(y, absdot, K, rounded_weights=False):
     return eh + half_step(np.abs(h) + eh)
 
 
-def combine_bound(y, absdot, idx, w, K, rounded_weights=False):
+def combine_bound(y, absdot, idx, w, K):
     T, top_k = idx.shape
-    e = product_bound(y, absdot, K, rounded_weights)
+    e = product_bound(y, absdot, K)
     out = np.zeros((T, y.shape[1]))
     mag = np.zeros_like(out)
     for t in range(T):
