@@ -113,6 +113,11 @@ struct Walk {
         ct = first % CT;
         locate();
     }
+    // tiles of this worker from here on
+    __device__ __forceinline__ int left(int workers) const {
+        const long long n = static_cast<long long>(tiles[E]) * CT - (static_cast<long long>(rt_all) * CT + ct);
+        return n <= 0 ? 0 : static_cast<int>((n + workers - 1) / workers);
+    }
     __device__ __forceinline__ bool done() const { return rt_all >= tiles[E]; }
     __device__ __forceinline__ void next() {
         rt_all += step_rt;
@@ -125,15 +130,12 @@ struct Walk {
     }
     __device__ __forceinline__ void locate() {
         if (done()) return;
-        int lo = e, hi = E;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (tiles[mid] <= rt_all) lo = mid; else hi = mid;
+        for (int n = 32; n == 32; e += n) {
+            const int i = e + 1 + (threadIdx.x & 31);
+            n = __popc(__ballot_sync(kFull, i < E && tiles[i] <= rt_all));
         }
-        e = lo;
-        const int first = (rt_all - tiles[lo]) * each[lo];
-        row0 = start[lo] + first;
-        nrows = min(each[lo], start[lo + 1] - row0);
+        row0 = start[e] + (rt_all - tiles[e]) * each[e];
+        nrows = min(each[e], start[e + 1] - row0);
     }
 };
 

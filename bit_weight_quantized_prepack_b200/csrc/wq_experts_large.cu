@@ -66,7 +66,7 @@ struct Ctl {
 
 // Arrive on the leader's barrier that lies where `bar` lies in this CTA. What the leader's MMAs
 // read is ordered by the proxy and tcgen05 fences before it, not by this arrival: one that releases
-// at cluster scope costs its thread some hundred cycles (up_prefill 366 us against 221).
+// at cluster scope costs its thread some hundred cycles (4096 tokens, 128 experts of 2048 x 1536: 366 us against 221).
 __device__ __forceinline__ void mbar_arrive_leader(uint64_t* bar) {
     asm volatile(
         "{\n\t.reg .b32 remote;\n\t"
@@ -162,7 +162,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
     __shared__ int s_start[kExMaxExperts + 1], s_tiles[kExMaxExperts + 1], s_each[kExMaxExperts], s_scratch[kLThreads / 32];
     __shared__ __align__(16) uint8_t stage_y[kAddWarps * kYBytes];
     __shared__ uint32_t s_tmem;
-    __shared__ int s_stop;
+    __shared__ int s_stop, s_rows_of[kStages];  // rows of the tile that a k-block belongs to
     const ExpertArgs& a = args.e;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_rank();  // 0: the leader, whose thread issues the pair's MMAs
@@ -239,6 +239,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
                 for (int i = 0; i < 8; ++i) row[j * 8 + i] = __shfl_sync(kFull, mine, i * 4 + sub);
             }
             const unsigned tile_n = n;
+            const int nrows = t.nrows;
             t.next();
             more = !t.done();
             bool read = false;
@@ -248,6 +249,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
                 const unsigned stage = n % kStages;
                 ok = __all_sync(kFull, wait_phase(&bars.empty[stage], ((n / kStages) & 1) ^ 1, ctl));
                 if (!ok) break;
+                if (lane == 0) s_rows_of[stage] = nrows;
                 const uint8_t* src = reinterpret_cast<const uint8_t*>(a.a + c * kTileK + piece * 8);
 #pragma unroll
                 for (int j = 0; j < kQuads; ++j)
@@ -282,20 +284,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
         if (rank == 0 && elect_one()) {
             // The thread's own instructions set the pace of small steps (a wait and a commit cost it about
             // 250 cycles, an MMA 15; probe): a wait per k-block, looked at while the one before is issued.
+            // A tile's rows come with its first k-block: to search the table cost one thread 2100 cycles a
+            // tile (4096 tokens, 8 of 128 experts: 2048 x 1536 281 us against 275, 768 x 2048 207 against 197).
             uint32_t stage = 0, ph = 0;
             unsigned m = 0;  // groups so far: sums m & 1
             bool ok = true;
             const uint64_t desc0 = smem_desc_sw128(smem_addr(ring));
-            bool more = !t.done();
             bool ready = mbar_test_wait(&bars.full[0], 0);
-            while (ok && more) {
-                const uint32_t idesc = idesc_f16_f32(2 * kColsL, (t.nrows + 15) / 16 * 16);
+            for (int left = t.left(gridDim.x / 2); ok && left > 0; --left) {
+                uint32_t idesc = 0;
                 int in_group = 0;  // k-blocks of the group that have been issued
                 for (int kb = 0; kb < KT; ++kb) {
                     if (SL < 2 && in_group == 0) ok = wait_phase(&bars.sum_empty[m & 1], ((m >> 1) & 1) ^ 1, ctl);
                     if (ok && !ready) ok = wait_phase(&bars.full[stage], ph, ctl);
                     if (!ok) break;
                     tc_fence_after();
+                    if (kb == 0) idesc = idesc_f16_f32(2 * kColsL, (*(volatile int*)&s_rows_of[stage] + 15) / 16 * 16);
                     const uint64_t db = smem_desc_advance(desc0, stage * kStageBytes);
                     const uint32_t wa = tmem + kTmemA + (stage % kSlotsA) * kChunkK;
                     constexpr int kGroups = SL < 2 ? 1 : SL;  // groups of a k-block
@@ -326,10 +330,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
                     stage = (stage + 1) % kStages;
                     ph ^= stage == 0;
                     ready = mbar_test_wait(&bars.full[stage], ph);
-                    if (kb == 0) {  // the next tile is found while this one is multiplied
-                        t.next();
-                        more = !t.done();
-                    }
                 }
             }
             // every MMA done before the CTA frees its tensor memory
