@@ -619,15 +619,15 @@ def _device_call(dev, stream, name, *args):
             _check(getattr(lib, name)(*args, handle), name)
 
 
-def _scratch(nbytes, dev, stream):
-    """Scratch of one call, allocated on the stream that the call runs on: it is handed out again
-    only to later work of that stream, and inside a graph capture it belongs to the graph."""
+def _new(shape, dtype, dev, stream):
+    """An output or scratch of one call, allocated on the stream that the call runs on: once freed, its
+    memory goes only to later work of that stream, and inside a graph capture it belongs to the graph."""
     if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        return torch.empty(shape, dtype=dtype, device=dev)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=dev)
     with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def _want(t, dtype, name, shape):
@@ -670,7 +670,7 @@ def wq_route_experts(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None
     _want(logits, dtype, "logits", (T, E))
     if score not in _SCORES:
         raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
-    if top_k <= 0:
+    if top_k <= 0 or top_k > E:
         raise WqError(WQ_ERR_INVALID_ARG, "wq_route_experts")
     if bias is not None:
         _want(bias, torch.float32, "bias", (E,))
@@ -680,11 +680,11 @@ def wq_route_experts(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None
         _want(w, torch.float32, "w", (T, top_k))
     dev = _one_device(logits, bias, idx, w, names=("logits", "bias", "idx", "w"))
     if idx is None:
-        idx = torch.empty(T, top_k, dtype=torch.int32, device=dev)
+        idx = _new((T, top_k), torch.int32, dev, stream)
     if w is None:
-        w = torch.empty(T, top_k, dtype=torch.float32, device=dev)
-    offsets = torch.empty(E + 1, dtype=torch.int32, device=dev) if lists else None
-    rows = torch.empty(T * top_k, dtype=torch.int32, device=dev) if lists else None
+        w = _new((T, top_k), torch.float32, dev, stream)
+    offsets = _new(E + 1, torch.int32, dev, stream) if lists else None
+    rows = _new(T * top_k, torch.int32, dev, stream) if lists else None
     _device_call(dev, stream, "wq_route_experts", logits.data_ptr(), int(dtype is torch.float32), _data(bias), T, E,
                  top_k, _SCORES[score], groups, top_groups, group_top, int(bool(renorm)), scale, idx.data_ptr(),
                  w.data_ptr(), _data(offsets), _data(rows))
@@ -703,9 +703,9 @@ def wq_expert_lists(idx: torch.Tensor, E: int, offsets: torch.Tensor | None = No
         _want(rows, torch.int32, "rows", (T * top_k,))
     dev = _one_device(idx, offsets, rows, names=("idx", "offsets", "rows"))
     if offsets is None:
-        offsets = torch.empty(max(E, 0) + 1, dtype=torch.int32, device=dev)
+        offsets = _new(max(E, 0) + 1, torch.int32, dev, stream)
     if rows is None:
-        rows = torch.empty(T * top_k, dtype=torch.int32, device=dev)
+        rows = _new(T * top_k, torch.int32, dev, stream)
     _device_call(dev, stream, "wq_expert_lists", idx.data_ptr(), T, E, top_k, offsets.data_ptr(), rows.data_ptr())
     return offsets, rows
 
@@ -740,7 +740,7 @@ def wq_prepack_experts(Q: torch.Tensor, s: torch.Tensor, g: int, gated: bool = F
         _tensor(Wp, torch.uint8, "Wp", min_numel=nbytes)
     dev = _one_device(Q, s, Wp, names=("Q", "s", "Wp"))
     if Wp is None:
-        Wp = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        Wp = _new(nbytes, torch.uint8, dev, stream)
     _device_call(dev, stream, "wq_prepack_experts", Q.data_ptr(), s.data_ptr(), E, K, N, g, int(bool(gated)),
                  Wp.data_ptr())
     return Wp
@@ -750,8 +750,8 @@ def wq_unpack_experts(Wp: torch.Tensor, E: int, K: int, N: int, g: int, gated: b
     """Inverse of wq_prepack_experts: (Q int32 [E, K/8, N], s fp16 [E, K/g, N])."""
     _tensor(Wp, torch.uint8, "Wp", min_numel=_experts_size(E, K, N, g, gated, "wq_unpack_experts"))
     dev = _one_device(Wp, names=("Wp",))
-    Q = torch.empty(E, K // 8, N, dtype=torch.int32, device=dev)
-    s = torch.empty(E, K // g, N, dtype=torch.float16, device=dev)
+    Q = _new((E, K // 8, N), torch.int32, dev, stream)
+    s = _new((E, K // g, N), torch.float16, dev, stream)
     _device_call(dev, stream, "wq_unpack_experts", Wp.data_ptr(), E, K, N, g, int(bool(gated)), Q.data_ptr(),
                  s.data_ptr())
     return Q, s
@@ -784,7 +784,7 @@ def wq_gemm_w4a16_experts(A: torch.Tensor, Wp: torch.Tensor, offsets: torch.Tens
         _want(Y, torch.float16, "Y", (pairs, n_out))
     dev = _one_device(A, Wp, offsets, rows, Y, names=("A", "Wp", "offsets", "rows", "Y"))
     if Y is None:
-        Y = torch.empty(pairs, n_out, dtype=torch.float16, device=dev)
+        Y = _new((pairs, n_out), torch.float16, dev, stream)
     if pairs:
         _device_call(dev, stream, "wq_gemm_w4a16_experts", A.data_ptr(), Wp.data_ptr(), offsets.data_ptr(),
                      rows.data_ptr(), Y.data_ptr(), T, E, pairs // T, N, K, g, int(bool(gated)))
@@ -817,10 +817,10 @@ def wq_gemm_w4a16_experts_combine(H: torch.Tensor, Wp: torch.Tensor, idx: torch.
     dev = _one_device(H, Wp, idx, w, offsets, rows, Y, scratch,
                       names=("H", "Wp", "idx", "w", "offsets", "rows", "Y", "scratch"))
     if Y is None:
-        Y = torch.empty(T, N, dtype=torch.float16, device=dev)
+        Y = _new((T, N), torch.float16, dev, stream)
     if pairs:
         if scratch is None and nbytes:
-            scratch = _scratch(nbytes, dev, stream)
+            scratch = _new(nbytes, torch.uint8, dev, stream)
         _device_call(dev, stream, "wq_gemm_w4a16_experts_combine", H.data_ptr(), Wp.data_ptr(), idx.data_ptr(),
                      w.data_ptr(), offsets.data_ptr(), rows.data_ptr(), Y.data_ptr(), _data(scratch),
                      0 if scratch is None else scratch.numel(), T, E, top_k, N, K, g)

@@ -258,3 +258,11 @@ def test_route_lists_and_prepack_refuse(rec):
     with pytest.raises(wq.WqError):
         wq.wq_prepack_experts(d["Q"], d["s"], 0)
     assert rec.calls == []
+
+
+@pytest.mark.parametrize("k", [9, 2 ** 30])
+def test_route_refuses_more_choices_than_experts(rec, k):
+    # before any output of that size is allocated
+    with pytest.raises(wq.WqError):
+        wq.wq_route_experts(torch.zeros((3, 8)), k)
+    assert rec.calls == []

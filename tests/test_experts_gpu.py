@@ -390,3 +390,62 @@ def test_empty_calls():
                                          torch.ones((3, 2), device="cuda"), off, rows, N, g)
     assert not Y.any()
     status_ok()
+
+
+def test_memory_of_a_side_stream_stays_with_it():
+    # what a call on another stream returned and the caller dropped must not be handed to the current
+    # stream while that other stream may still write it
+    x = torch.randn((4096, 256), device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for stream in (s, s.cuda_stream):
+        out = wq.wq_route_experts(x, 8, lists=True, stream=stream)
+        held = {t.data_ptr() for t in out}
+        shapes = [(t.shape, t.dtype) for t in out]
+        del out
+        fresh = [torch.empty(shape, dtype=dtype, device="cuda") for shape, dtype in shapes]
+        assert not held & {t.data_ptr() for t in fresh}
+    torch.cuda.synchronize()
+    status_ok()
+
+
+def test_layers_and_a_dense_product_at_the_same_time():
+    # few pairs, few rows, many rows and a dense layer on four streams, unordered among each other
+    runs = [_layer(T, 8, 2, 512, 256, 128, seed=T)[-1] for T in (1, 40, 700)]
+    d = experts_inputs(1, 512, 2048, 128, 1, 1, seed=3)
+    Wd = wq.wq_prepack(dev(d["Q"][0]), dev(d["s"][0]), 128)
+    A = torch.randn((96, 512), device="cuda").half()
+    runs.append(lambda stream=None: (wq.wq_gemm_w4a16(A, Wd, 2048, 128, stream=stream),))
+    want = [r()[0].clone() for r in runs]
+    streams = [torch.cuda.Stream() for _ in runs]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(20):
+        for i, (r, st) in enumerate(zip(runs, streams)):
+            with torch.cuda.stream(st):
+                outs.append((i, r(stream=st)[0]))
+    torch.cuda.synchronize()
+    for i, y in outs:
+        assert torch.equal(y, want[i])
+    status_ok()
+
+
+@pytest.mark.parametrize("T", [1, 30, 400])
+def test_the_same_expert_twice(T):
+    # choices of one token that name the same expert are pairs of their own
+    E, K, N, g, k = 6, 384, 72, 128, 3
+    d = experts_inputs(E, K, N, g, T, k, seed=T)
+    idx = d["idx"].copy()
+    idx[:, 1] = idx[:, 0]
+    idx[::2, 2] = idx[::2, 0]
+    w = np.random.default_rng(T).uniform(0.1, 1.0, (T, k)).astype(np.float32)
+    H = (np.random.default_rng(T + 1).standard_normal((T * k, K)) * 0.5).astype(np.float16)
+    Wp = wq.wq_prepack_experts(dev(d["Q"]), dev(d["s"]), g)
+    offsets, rows = wq.wq_expert_lists(dev(idx), E)
+    o_ref, r_ref = oracle.expert_lists(idx, E)
+    assert np.array_equal(offsets.cpu().numpy(), o_ref) and np.array_equal(rows.cpu().numpy(), r_ref)
+    y = wq.wq_gemm_w4a16_experts_combine(dev(H), Wp, dev(idx), dev(w), offsets, rows, N, g)
+    v, vad = oracle.experts_product(H.astype(np.float64), d["Q"], d["s"], g, idx, by_pair=True)
+    ref = oracle.experts_combine(v, idx, w.astype(np.float64))
+    assert np.all(np.abs(f64(y) - ref) <= combine_bound(v, vad, idx, w.astype(np.float64), K))
+    status_ok()
