@@ -424,7 +424,6 @@ int acquire_device(cudaStream_t stream, DeviceInfo* info) {
     }
     info->num_sms = d->num_sms;
     info->status = d->status;
-    info->encode = reinterpret_cast<void*>(g_encode);
     info->timeout_ns = g_timeout_ns;
     return WQ_OK;
 }

@@ -49,7 +49,6 @@ inline size_t ex_expert_stride(int K, int N, int g) {
 struct DeviceInfo {
     int num_sms;
     int* status;                    // device status word
-    void* encode;                   // cuTensorMapEncodeTiled
     unsigned long long timeout_ns;  // limit of every device-side wait
 };
 int acquire_device(cudaStream_t stream, DeviceInfo* info);
