@@ -9,13 +9,14 @@
 // bits, and only the other tokens (one in some hundred for random scores) are done again in 64.
 // Keys are mapped to unsigned integers of the same order, so that a warp's maximum is one reduction
 // instruction per 32 bits; among equal keys the lowest expert wins. An expert whose logit or bias is
-// not finite has key 0, below every finite one, and is never chosen.
+// not finite has key 0, below every finite one, and is never chosen. Bound by the integer pipe (65 % at
+// 8192 tokens of 256 experts with groups: 20 us for 8.4 MB of logits).
 //
 // lists_kernel: one CTA per two experts. Every CTA reads all choices: a thread counts those of lower
 // experts (the place in `rows` where its experts begin) and notes, a bit per choice and expert, which
 // are its experts' own; the pairs are then written from the notes, in order, the places of up to
 // eight steps from one sum over the lanes where an expert is in many of them (one step after
-// another, the busiest expert's CTA took 16 us of 65536 choices over 256 experts, now 11). No
+// another, the lists of 65536 choices over 256 experts took 16 us, now 11). No
 // atomics and no scratch: the lists are the same every time. Bound by the count and notes of every
 // choice in every CTA, hence two experts to each. Up to kFuseTokens tokens the routing and the lists
 // are one launch of one CTA, with a thread per expert.
@@ -187,14 +188,16 @@ __device__ __noinline__ int route64(const RouteArgs a, int t, double top, double
     return mine;
 }
 
-// The choice by 32-bit keys, those of the experts that stay. Lane j returns the j-th choice; *place
-// its key, lane top_k the key behind the last choice (with `next`).
+// The choice by 32-bit keys, those of the experts that stay: one expert after another, the lowest index
+// first among equal keys.
 template <int VPL>
-__device__ __forceinline__ int choose32(unsigned (&key)[VPL], int top_k, bool next, unsigned* place) {
+__device__ __forceinline__ int choose_each(const unsigned (&keys)[VPL], int top_k, int steps, unsigned* place) {
     const int lane = threadIdx.x & 31;
+    unsigned key[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] = keys[i];
     int mine = -1;
     *place = 0;
-    const int steps = next && top_k < 32 ? top_k + 1 : top_k;
 #pragma unroll 1
     for (int j = 0; j < steps; ++j) {
         unsigned lk = key[0];
@@ -216,6 +219,70 @@ __device__ __forceinline__ int choose32(unsigned (&key)[VPL], int top_k, bool ne
             if (i * 32 + lane == e) key[i] = 0u;
     }
     return mine;
+}
+
+template <int VPL>
+__device__ __noinline__ int choose_ties(const unsigned (&keys)[VPL], int top_k, int steps, unsigned* place) {
+    return choose_each<VPL>(keys, top_k, steps, place);
+}
+
+// The choice by 32-bit keys. Lane j returns the j-th choice; *place its key, lane top_k the key
+// behind the last choice, where `next` asks for it. With 8 keys a lane or more, every lane sorts its keys once, so that a
+// choice is the largest of the lanes' first keys and a step of one lane's list; the index is looked
+// up at the end, by all lanes at once. Two equal keys, which this way come out one after the other
+// (the last one's equal as the key behind it, or, with 32 choices, in another lane or next in the
+// list), are left to the loop above. 8192 tokens of 256 experts: 30.6 us with the lists against 32.8;
+// with 2 or 4 keys a lane the loop is as fast or faster (1000 tokens of 60 experts 6.9 us, sorted 7.2).
+template <int VPL>
+__device__ __forceinline__ int choose32(const unsigned (&key)[VPL], int top_k, bool next, unsigned* place) {
+    const int lane = threadIdx.x & 31;
+    const int steps = top_k < 32 ? top_k + 1 : top_k;
+    if constexpr (VPL < 8) return choose_each<VPL>(key, top_k, next ? steps : top_k, place);
+    unsigned s[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) s[i] = key[i];
+#pragma unroll
+    for (int size = 2; size <= VPL; size *= 2)  // bitonic, descending
+#pragma unroll
+        for (int stride = size / 2; stride; stride /= 2)
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if ((i & stride) == 0) {
+                    const unsigned x = s[i], y = s[i + stride];
+                    const bool down = (i & size) == 0;
+                    s[i] = down ? max(x, y) : min(x, y);
+                    s[i + stride] = down ? min(x, y) : max(x, y);
+                }
+    unsigned last = 0u;
+    int who = 0;
+    bool tie = false;
+    *place = 0;
+#pragma unroll 1
+    for (int j = 0; j < steps; ++j) {
+        const unsigned best = __reduce_max_sync(kFull, s[0]);
+        if (best == 0u) break;
+        tie |= best == last;
+        last = best;
+        const unsigned holders = __ballot_sync(kFull, s[0] == best);
+        const int w = __ffs(holders) - 1;
+        tie |= j == 31 && (holders & (holders - 1u)) != 0u;
+        if (lane == j) {
+            *place = best;
+            who = w;
+        }
+        if (lane == w) {
+#pragma unroll
+            for (int i = 0; i + 1 < VPL; ++i) s[i] = s[i + 1];
+            s[VPL - 1] = 0u;
+        }
+    }
+    if (top_k == 32) tie |= __any_sync(kFull, last != 0u && s[0] == last);
+    if (tie) return choose_ties<VPL>(key, top_k, steps, place);
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+        if (__shfl_sync(kFull, key[i], who) == *place) mine = i * 32 + who;
+    return lane < top_k && *place ? mine : -1;
 }
 
 // The 32-bit choice may hold the right experts in the wrong order, or miss one by a hair: all experts
@@ -358,9 +425,7 @@ __device__ __forceinline__ bool route32(const RouteArgs& a, int t, const Row<VPL
         __syncwarp();
     }
     if (close) return false;
-    unsigned mk, was[VPL];
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) was[i] = key[i];
+    unsigned mk;
     *mine = choose32<VPL>(key, a.top_k, a.bias != nullptr, &mk);
     if (!a.bias) return true;
     const unsigned after = __shfl_down_sync(kFull, mk, 1);
@@ -373,7 +438,7 @@ __device__ __forceinline__ bool route32(const RouteArgs& a, int t, const Row<VPL
     unsigned within = 0;
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-        if (was[i] && too_close(last, value_of(was[i]), 1.0f, err)) within |= 1u << i;
+        if (key[i] && too_close(last, value_of(key[i]), 1.0f, err)) within |= 1u << i;
     return resolve64<VPL>(a, t, static_cast<double>(top), within, scratch, mine);
 }
 
