@@ -4,14 +4,17 @@
 //
 // experts_kernel (few rows per expert). Tile: 32 columns of one expert x up to 8 of its rows, all of
 // K. A CTA has an equal run of all tiles, as segments of one row tile each, whose rows it keeps
-// in shared memory. Each of its 16 warps has an equal run of a segment's k-blocks (tile after tile,
-// 2 KiB of codes each, contiguous in memory) and streams them, across segments, into registers: 16
-// bytes a lane, a whole fragment of the weight. The weight is the 16-row operand of m16n8k16 (exact
-// fp16 q - 8), the tokens are its 8 columns; each scale multiplies its fp32 partial, so no weight is
-// rounded. A tile whose k-blocks lie with several warps is summed by the one that has the first, in
-// the order of the warps. Bound by HBM in the limit; the rows stay in shared memory because every SM
-// wants the same few at the same time: through a ring per warp, past L1, up_wide took 148 us, with L1
-// 85.
+// in shared memory. Each of its 24 warps (16 where the rows are long) has an equal run of a segment's
+// k-blocks (tile after tile, 2 KiB of codes each, contiguous in memory) and streams them, across
+// segments, into registers: 16 bytes a lane, a whole fragment of the weight. The weight is the 16-row
+// operand of m16n8k16 (exact fp16 q - 8), the tokens are its 8 columns; each scale multiplies its
+// fp32 partial, so no weight is rounded. A tile whose k-blocks lie with several warps is summed by the
+// one that has the first, in the order of the warps. The rows stay in shared memory because every SM
+// wants the same few at the same time: through a ring per warp 16 tokens over 2 of 8 experts of 4096 x
+// 22016 took 148 us, with the ring filled through L1 85. Now 72.6 us, 357 MB at 4.9 TB/s; 24 tokens
+// over 6 of 60 of 4096 x 1400, g = 64: 42 us, 167 MB at 4.0 TB/s. Without rows and MMAs the streams
+// reach 0.80 to 0.89 of the copy rate; the rest is the dequantisation's instructions, which grow with
+// the scales of a k-block.
 #include <cuda_runtime.h>
 #include <cuda_fp16.h>
 #include <cstdint>
@@ -25,7 +28,7 @@ namespace wq {
 namespace {
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-    // through L1: the warps of a CTA want the same rows at about the same time
+    // through L1: neighbouring tiles want the same rows
     asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -54,8 +57,9 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// SL: scales per k-block and column (1, 2 or 4 groups of a k-block; 0: per-column, g == K). W: warps. With one k-block ahead of the one in hand, 24 warps of 80 registers
-// hide more than 16 of 128 with three (up_wide 72.6 us against 84.4; 28 warps 74.6, 32 76.5).
+// SL: scales per k-block and column (1, 2 or 4 groups of a k-block; 0: per-column, g == K). W: warps.
+// With one k-block ahead of the one in hand, 24 warps of 80 registers hide more than 16 of 128 with
+// three (16 tokens, 2 of 8 experts of 4096 x 22016: 72.6 us against 84.4; 28 warps 74.6, 32 76.5).
 template <int SL_, int W_>
 struct Small {
     static constexpr int SL = SL_, W = W_;
@@ -323,7 +327,9 @@ __global__ void __launch_bounds__(C::W * 32, 1) experts_kernel(ExpertArgs a, int
 // in fp32. It saves a launch, the pairs' sums through memory and a rounding of each. Otherwise row i
 // is place i of the lists; its expert ends at the first offset above i.
 // An expert that two rows share is read twice (the second time from L2), which is what limits this
-// form to few pairs.
+// form to few pairs. Bound by latency: one token over 8 of 128 experts, gated 2048 x 1536: 8.1 us for
+// 13 MB, combined 768 x 2048: 6.6 us for 6.5 MB, of which an empty kernel takes 2.5; the 8-row tiles
+// with their table took 12 and 10.8.
 template <int SL, bool kSum>
 __global__ void __launch_bounds__(512, 1) experts_token_kernel(ExpertArgs a, const int32_t* __restrict__ idx,
                                                                const float* __restrict__ wt, int top_k, int WK) {
@@ -506,7 +512,8 @@ __global__ void __launch_bounds__(512, 1) experts_token_kernel(ExpertArgs a, con
 
 // Y[t] = sum over j of w[t, j] * yp[t * top_k + j], in the order of j, fp32; a choice outside
 // [0, E) adds nothing and its row is not read. One thread per 8 columns of a token, four choices'
-// rows under way at a time. Bound by the pairs' bytes (down_prefill: 134 MB of pairs in 26 us).
+// rows under way at a time. Bound by the pairs' bytes: 4096 tokens, 8 choices
+// of 2048 columns, 134 MB read and 17 MB written in 28 us, 5.4 TB/s.
 __global__ void __launch_bounds__(256) combine_kernel(const uint16_t* __restrict__ yp, const int32_t* __restrict__ idx,
                                                       const float* __restrict__ w, int top_k, int E, int N,
                                                       uint16_t* __restrict__ Y, long long total) {

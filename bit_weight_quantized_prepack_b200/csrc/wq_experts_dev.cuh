@@ -95,7 +95,8 @@ __device__ void rows_per_tile(int E, int unit, const int* s_start, const int* s_
 }
 
 // Walk of worker `first` of `workers` over the tiles: row tile rt_all of all experts' row tiles, column
-// tile ct of CT; the column tiles of one row tile are neighbours.
+// tile ct of CT; the column tiles of one row tile are neighbours. next() is for whole warps: its search
+// looks at 32 experts at a time.
 struct Walk {
     int rt_all, ct, e;       // position
     int row0, nrows;         // rows of the tile: places row0 .. of the lists
