@@ -619,15 +619,19 @@ def _device_call(dev, stream, name, *args):
             _check(getattr(lib, name)(*args, handle), name)
 
 
-def _new(shape, dtype, dev, stream):
-    """An output or scratch of one call, allocated on the stream that the call runs on: once freed, its
-    memory goes only to later work of that stream, and inside a graph capture it belongs to the graph."""
+def _empty_on(stream, dev):
+    """torch.empty for the outputs and the scratch of one call, on the stream that the call runs on: once
+    freed, their memory goes only to later work of that stream, and inside a graph capture it belongs
+    to the graph."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=dev)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+
+    def empty(*shape, **kw):
+        with torch.cuda.stream(stream):
+            return torch.empty(*shape, **kw)
+    return empty
 
 
 def _want(t, dtype, name, shape):
@@ -679,12 +683,13 @@ def wq_route_experts(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None
     if w is not None:
         _want(w, torch.float32, "w", (T, top_k))
     dev = _one_device(logits, bias, idx, w, names=("logits", "bias", "idx", "w"))
+    empty = _empty_on(stream, dev)
     if idx is None:
-        idx = _new((T, top_k), torch.int32, dev, stream)
+        idx = empty(T, top_k, dtype=torch.int32, device=dev)
     if w is None:
-        w = _new((T, top_k), torch.float32, dev, stream)
-    offsets = _new(E + 1, torch.int32, dev, stream) if lists else None
-    rows = _new(T * top_k, torch.int32, dev, stream) if lists else None
+        w = empty(T, top_k, dtype=torch.float32, device=dev)
+    offsets = empty(E + 1, dtype=torch.int32, device=dev) if lists else None
+    rows = empty(T * top_k, dtype=torch.int32, device=dev) if lists else None
     _device_call(dev, stream, "wq_route_experts", logits.data_ptr(), int(dtype is torch.float32), _data(bias), T, E,
                  top_k, _SCORES[score], groups, top_groups, group_top, int(bool(renorm)), scale, idx.data_ptr(),
                  w.data_ptr(), _data(offsets), _data(rows))
@@ -702,10 +707,11 @@ def wq_expert_lists(idx: torch.Tensor, E: int, offsets: torch.Tensor | None = No
     if rows is not None:
         _want(rows, torch.int32, "rows", (T * top_k,))
     dev = _one_device(idx, offsets, rows, names=("idx", "offsets", "rows"))
+    empty = _empty_on(stream, dev)
     if offsets is None:
-        offsets = _new(max(E, 0) + 1, torch.int32, dev, stream)
+        offsets = empty(max(E, 0) + 1, dtype=torch.int32, device=dev)
     if rows is None:
-        rows = _new(T * top_k, torch.int32, dev, stream)
+        rows = empty(T * top_k, dtype=torch.int32, device=dev)
     _device_call(dev, stream, "wq_expert_lists", idx.data_ptr(), T, E, top_k, offsets.data_ptr(), rows.data_ptr())
     return offsets, rows
 
@@ -739,8 +745,9 @@ def wq_prepack_experts(Q: torch.Tensor, s: torch.Tensor, g: int, gated: bool = F
     if Wp is not None:
         _tensor(Wp, torch.uint8, "Wp", min_numel=nbytes)
     dev = _one_device(Q, s, Wp, names=("Q", "s", "Wp"))
+    empty = _empty_on(stream, dev)
     if Wp is None:
-        Wp = _new(nbytes, torch.uint8, dev, stream)
+        Wp = empty(nbytes, dtype=torch.uint8, device=dev)
     _device_call(dev, stream, "wq_prepack_experts", Q.data_ptr(), s.data_ptr(), E, K, N, g, int(bool(gated)),
                  Wp.data_ptr())
     return Wp
@@ -750,8 +757,9 @@ def wq_unpack_experts(Wp: torch.Tensor, E: int, K: int, N: int, g: int, gated: b
     """Inverse of wq_prepack_experts: (Q int32 [E, K/8, N], s fp16 [E, K/g, N])."""
     _tensor(Wp, torch.uint8, "Wp", min_numel=_experts_size(E, K, N, g, gated, "wq_unpack_experts"))
     dev = _one_device(Wp, names=("Wp",))
-    Q = _new((E, K // 8, N), torch.int32, dev, stream)
-    s = _new((E, K // g, N), torch.float16, dev, stream)
+    empty = _empty_on(stream, dev)
+    Q = empty(E, K // 8, N, dtype=torch.int32, device=dev)
+    s = empty(E, K // g, N, dtype=torch.float16, device=dev)
     _device_call(dev, stream, "wq_unpack_experts", Wp.data_ptr(), E, K, N, g, int(bool(gated)), Q.data_ptr(),
                  s.data_ptr())
     return Q, s
@@ -783,8 +791,9 @@ def wq_gemm_w4a16_experts(A: torch.Tensor, Wp: torch.Tensor, offsets: torch.Tens
     if Y is not None:
         _want(Y, torch.float16, "Y", (pairs, n_out))
     dev = _one_device(A, Wp, offsets, rows, Y, names=("A", "Wp", "offsets", "rows", "Y"))
+    empty = _empty_on(stream, dev)
     if Y is None:
-        Y = _new((pairs, n_out), torch.float16, dev, stream)
+        Y = empty(pairs, n_out, dtype=torch.float16, device=dev)
     if pairs:
         _device_call(dev, stream, "wq_gemm_w4a16_experts", A.data_ptr(), Wp.data_ptr(), offsets.data_ptr(),
                      rows.data_ptr(), Y.data_ptr(), T, E, pairs // T, N, K, g, int(bool(gated)))
@@ -816,11 +825,12 @@ def wq_gemm_w4a16_experts_combine(H: torch.Tensor, Wp: torch.Tensor, idx: torch.
         _tensor(scratch, torch.uint8, "scratch", min_numel=nbytes)
     dev = _one_device(H, Wp, idx, w, offsets, rows, Y, scratch,
                       names=("H", "Wp", "idx", "w", "offsets", "rows", "Y", "scratch"))
+    empty = _empty_on(stream, dev)
     if Y is None:
-        Y = _new((T, N), torch.float16, dev, stream)
+        Y = empty(T, N, dtype=torch.float16, device=dev)
     if pairs:
         if scratch is None and nbytes:
-            scratch = _new(nbytes, torch.uint8, dev, stream)
+            scratch = empty(nbytes, dtype=torch.uint8, device=dev)
         _device_call(dev, stream, "wq_gemm_w4a16_experts_combine", H.data_ptr(), Wp.data_ptr(), idx.data_ptr(),
                      w.data_ptr(), offsets.data_ptr(), rows.data_ptr(), Y.data_ptr(), _data(scratch),
                      0 if scratch is None else scratch.numel(), T, E, top_k, N, K, g)
