@@ -218,7 +218,9 @@ __global__ void __launch_bounds__(C::W * 32, 1) experts_kernel(ExpertArgs a, int
             for (int m = 0; m < g.nrows; ++m) {
                 const float out = value(m, lane) * c0;
                 const int p = s_pair[place][m];
-                if (n < n_out && p >= 0) a.y[static_cast<size_t>(p) * n_out + n] = __half_as_ushort(__float2half_rn(out));
+                if (n >= n_out || p < 0) continue;
+                const size_t at = static_cast<size_t>(p) * n_out + n;
+                if (a.y32) a.y32[at] = out; else a.y[at] = __half_as_ushort(__float2half_rn(out));
             }
         }
     };
@@ -511,18 +513,19 @@ __global__ void __launch_bounds__(512, 1) experts_token_kernel(ExpertArgs a, con
 }
 
 // Y[t] = sum over j of w[t, j] * yp[t * top_k + j], in the order of j, fp32; a choice outside
-// [0, E) adds nothing and its row is not read. One thread per 8 columns of a token, four choices'
-// rows under way at a time. Bound by the pairs' bytes: 4096 tokens, 8 choices
-// of 2048 columns, 134 MB read and 17 MB written in 28 us, 5.4 TB/s.
-__global__ void __launch_bounds__(256) combine_kernel(const uint16_t* __restrict__ yp, const int32_t* __restrict__ idx,
+// [0, E) adds nothing and its row is not read. The pairs' products come unrounded: a rounding of each
+// to fp16 would add to the output's own (1.4 times as far from the exact sum), and a product beyond
+// 65504 would be lost although its weighted sum is finite. One thread per 4 columns of a token, four
+// choices' rows under way at a time. Bound by the pairs' bytes.
+__global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ yp, const int32_t* __restrict__ idx,
                                                       const float* __restrict__ w, int top_k, int E, int N,
                                                       uint16_t* __restrict__ Y, long long total) {
     const long long i = blockIdx.x * 256ll + threadIdx.x;
     if (i >= total) return;
-    const int per_row = N / 8;
+    const int per_row = N / 4;
     const long long t = i / per_row;
-    const int n = static_cast<int>(i - t * per_row) * 8;
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const int n = static_cast<int>(i - t * per_row) * 4;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
     for (int j0 = 0; j0 < top_k; j0 += 4) {
         uint4 v[4];
         float wj[4];
@@ -539,20 +542,17 @@ __global__ void __launch_bounds__(256) combine_kernel(const uint16_t* __restrict
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             if (!in[j]) continue;
-            const __half2* h = reinterpret_cast<const __half2*>(&v[j]);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 f = __half22float2(h[k]);
-                acc[2 * k] += wj[j] * f.x;
-                acc[2 * k + 1] += wj[j] * f.y;
-            }
+            acc[0] += wj[j] * __uint_as_float(v[j].x);
+            acc[1] += wj[j] * __uint_as_float(v[j].y);
+            acc[2] += wj[j] * __uint_as_float(v[j].z);
+            acc[3] += wj[j] * __uint_as_float(v[j].w);
         }
     }
-    uint4 out;
+    uint2 out;
     __half2* o = reinterpret_cast<__half2*>(&out);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) o[k] = __floats2half2_rn(acc[2 * k], acc[2 * k + 1]);
-    *reinterpret_cast<uint4*>(Y + t * N + n) = out;
+    o[0] = __floats2half2_rn(acc[0], acc[1]);
+    o[1] = __floats2half2_rn(acc[2], acc[3]);
+    *reinterpret_cast<uint2*>(Y + t * N + n) = out;
 }
 
 template <class C>
@@ -646,9 +646,9 @@ cudaError_t launch_experts(const ExpertArgs& a, const DeviceInfo& d, cudaStream_
     return launch_w<16>(a, d.num_sms, st);
 }
 
-cudaError_t launch_combine_experts(const uint16_t* yp, const int32_t* idx, const float* w, int T, int top_k, int E,
+cudaError_t launch_combine_experts(const float* yp, const int32_t* idx, const float* w, int T, int top_k, int E,
                                    int N, uint16_t* Y, cudaStream_t st) {
-    const long long total = static_cast<long long>(T) * (N / 8);
+    const long long total = static_cast<long long>(T) * (N / 4);
     combine_kernel<<<static_cast<unsigned>((total + 255) / 256), 256, 0, st>>>(yp, idx, w, top_k, E, N, Y, total);
     return cudaGetLastError();
 }

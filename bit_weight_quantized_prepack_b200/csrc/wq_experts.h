@@ -72,6 +72,7 @@ struct ExpertArgs {
     const int32_t* offsets;    // [E + 1]
     const int32_t* rows;       // [pairs]
     uint16_t* y;               // [pairs, n_out]
+    float* y32;                // not null: the products go here instead, not rounded to fp16 (gated 0)
     int* status;               // device status word
     size_t expert_stride, scale_offset;
     int pairs, a_div;          // pair p reads row p / a_div of a
@@ -98,7 +99,7 @@ bool experts_token_form(int pairs, int E);
 // Y of args: [tokens, N]; a_div 1.
 cudaError_t launch_experts_token(const ExpertArgs& a, const int32_t* idx, const float* w, int top_k, int num_sms,
                                  cudaStream_t st);
-cudaError_t launch_combine_experts(const uint16_t* yp, const int32_t* idx, const float* w, int T, int top_k, int E,
+cudaError_t launch_combine_experts(const float* yp, const int32_t* idx, const float* w, int T, int top_k, int E,
                                    int N, uint16_t* Y, cudaStream_t st);
 
 }  // namespace wq

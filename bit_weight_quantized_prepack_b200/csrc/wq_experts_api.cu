@@ -174,7 +174,7 @@ int wq_gemm_w4a16_experts(const uint16_t* A, const void* Wp, const int32_t* offs
 
 size_t wq_experts_scratch_bytes(int T, int E, int top_k, int N) {
     if (check_counts(T, E, top_k) != WQ_OK || N <= 0 || N % 8 || experts_token_form(T * top_k, E)) return 0;
-    return static_cast<size_t>(T) * top_k * N * 2;
+    return static_cast<size_t>(T) * top_k * N * sizeof(float);
 }
 
 int wq_gemm_w4a16_experts_combine(const uint16_t* H, const void* Wp, const int32_t* idx, const float* w,
@@ -193,19 +193,20 @@ int wq_gemm_w4a16_experts_combine(const uint16_t* H, const void* Wp, const int32
     if (!aligned(H, 16) || !aligned(Y, 16) || !aligned(scratch, 16) || !aligned(idx, 4) || !aligned(w, 4))
         return WQ_ERR_MISALIGNED;
     if (scratch_bytes < need) return WQ_ERR_INVALID_ARG;
-    // one thread of the summing kernel per 8 columns of a token
-    if (static_cast<long long>(T) * (N / 8) >= (1ll << 31) * 128) return WQ_ERR_UNSUPPORTED_SHAPE;
+    // one thread of the summing kernel per 4 columns of a token
+    if (static_cast<long long>(T) * (N / 4) >= (1ll << 31) * 128) return WQ_ERR_UNSUPPORTED_SHAPE;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     DeviceInfo d;
     rc = acquire_device(st, &d);
     if (rc) return rc;
-    uint16_t* yp = static_cast<uint16_t*>(scratch);
     if (experts_token_form(T * top_k, E))
         return status_of(launch_experts_token(product_args(H, Wp, offsets, rows, Y, T, E, top_k, 1, N, K, g, 0, d), idx, w,
                                               top_k, d.num_sms, st));
-    rc = status_of(launch_experts(product_args(H, Wp, offsets, rows, yp, T, E, top_k, 1, N, K, g, 0, d), d, st));
+    ExpertArgs a = product_args(H, Wp, offsets, rows, nullptr, T, E, top_k, 1, N, K, g, 0, d);
+    a.y32 = static_cast<float*>(scratch);
+    rc = status_of(launch_experts(a, d, st));
     if (rc) return rc;
-    return status_of(launch_combine_experts(yp, idx, w, T, top_k, E, N, Y, st));
+    return status_of(launch_combine_experts(a.y32, idx, w, T, top_k, E, N, Y, st));
 }
 
 }  // extern "C"

@@ -504,6 +504,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
                     const int n = ct * (kColsL / 2) + quarter * 16 + (lane & 1) * 8;
                     const uint4 v4 = *reinterpret_cast<const uint4*>(out + (lane >> 1) * kYRowGated + (lane & 1) * 16);
                     if (p >= 0 && n < n_out) *reinterpret_cast<uint4*>(a.y + static_cast<size_t>(p) * n_out + n) = v4;
+                } else if (a.y32) {
+                    // 8 rows x 32 columns at a time, a row of 128 bytes
+                    float* col = reinterpret_cast<float*>(out) + lane;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        if (k) __syncwarp();
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) col[r * 32] = acc[i][k * 8 + r];
+                        __syncwarp();
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const int row = q * 4 + (lane >> 3);
+                            const int p = __shfl_sync(kFull, p_row, k * 8 + row);
+                            const int n = ct * kColsL + quarter * 32 + (lane & 7) * 4;
+                            const uint4 v4 = *reinterpret_cast<const uint4*>(out + row * 128 + (lane & 7) * 16);
+                            if (p >= 0 && n < n_out) *reinterpret_cast<uint4*>(a.y32 + static_cast<size_t>(p) * n_out + n) = v4;
+                        }
+                    }
                 } else {
                     uint16_t* col = reinterpret_cast<uint16_t*>(out) + lane;
 #pragma unroll

@@ -326,10 +326,10 @@ WQ_API int wq_gemm_w4a16_noalloc(const uint16_t* A, const void* Wp, uint16_t* Y,
  * wq_gemm_w4a16_experts_combine: Y[t, n] = sum over j of w[t, j] * (H[t * top_k + j] . W_e[:, n]),
  * e = idx[t, j]; choices outside [0, E) add nothing (a token without any gets zeros). H fp16
  * [T * top_k, K] by pair, Y fp16 [T, N], and idx, w and the lists as wq_route_experts gives them
- * (the lists are those of idx). The sum is fp32: of each pair's product rounded to fp16, over j in
- * order, or for few pairs (T * top_k <= E / 4) of the unrounded products. scratch:
- * wq_experts_scratch_bytes(T, E, top_k, N) bytes that the call may write until it has completed (0
- * for few pairs: it may then be null). Y and scratch must overlap neither each other nor an input. */
+ * (the lists are those of idx). Every pair's product and the sum over j are fp32, Y is rounded
+ * once. scratch: wq_experts_scratch_bytes(T, E, top_k, N) bytes, the fp32 products, that the call may
+ * write until it has completed (0 for few pairs, T * top_k <= E / 4: it may then be null). Y and
+ * scratch must overlap neither each other nor an input. */
 WQ_API int wq_route_experts(const void* logits, int logits_fp32, const float* bias, int T, int E, int top_k, int score,
                  int groups, int top_groups, int group_top, int renorm, float scale, int32_t* idx, float* w,
                  int32_t* offsets, int32_t* rows, void* stream);

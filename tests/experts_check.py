@@ -71,3 +71,23 @@ def experts_inputs(E, K, N, g, T, top_k, seed=0, padded=0.0, by_pair=False, skew
     offsets, rows = oracle.expert_lists(idx, E)
     rows = np.concatenate([rows, np.full(T * top_k - rows.size, -12345, dtype=np.int32)]).astype(np.int32)
     return {"Q": Q, "s": s, "A": A, "idx": idx, "w": w, "offsets": offsets, "rows": rows}
+
+
+def combine_bound_once(y, absdot, idx, w, K):
+    """The weighted sum with one rounding, the output's: the pairs' products enter as fp32 sums.
+
+    A pair's sum as in sum_bound, its scale times w one rounding more (2^-24). The sum over the choices:
+    top_k products and additions of 2^-24 of the magnitudes each; where the choices' k-blocks are added to
+    one running sum, at most K/32 additions a choice (a scale per 32 rows) of 2^-24 of all that is
+    in the sum, for top_k choices."""
+    T, top_k = idx.shape
+    err, mag, out = np.zeros((T, y.shape[1])), np.zeros((T, y.shape[1])), np.zeros((T, y.shape[1]))
+    for t in range(T):
+        for j in range(top_k):
+            p = t * top_k + j
+            if not np.isnan(y[p]).all():
+                out[t] += float(w[t, j]) * y[p]
+                err[t] += abs(float(w[t, j])) * (sum_bound(y[p], absdot[p], K) + 2.0 ** -24 * absdot[p])
+                mag[t] += abs(float(w[t, j])) * absdot[p]
+    err = err + 2.0 ** -24 * (2 * top_k + top_k * K / 32) * mag
+    return err + half_step(np.abs(out) + err)

@@ -1,0 +1,47 @@
+"""GPU tests of the expert operators at their edges, against the fp64 oracle."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
+
+import bit_weight_quantized_prepack_b200 as wq  # noqa: E402
+import oracle  # noqa: E402
+from experts_check import combine_bound_once, experts_inputs  # noqa: E402
+
+
+def dev(x):
+    return torch.from_numpy(np.ascontiguousarray(x)).cuda()
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+# ------------------------------------------------------------------ the combined product rounds once
+@pytest.mark.parametrize("large", [False, True])
+@pytest.mark.parametrize("E,K,N,g,T,k,padded", [
+    (64, 768, 264, 128, 1, 8, 0), (40, 1280, 72, 640, 5, 2, 0.4), (33, 384, 48, 32, 2, 4, 0),           # few pairs
+    (8, 1024, 272, 128, 3, 2, 0), (6, 640, 112, 64, 13, 4, 0.3), (4, 512, 96, 512, 20, 2, 0),            # few rows
+    (5, 384, 80, 32, 40, 3, 0.2),
+    (2, 512, 272, 128, 128, 1, 0), (3, 640, 528, 64, 200, 2, 0.1), (2, 384, 96, 384, 90, 2, 0),          # many rows
+    (4, 256, 1040, 32, 260, 4, 0.1)])
+def test_combine_rounds_once(E, K, N, g, T, k, padded, large):
+    d = experts_inputs(E, K, N, g, T, k, seed=E * 3 + T, padded=padded, by_pair=True)
+    s, w = d["s"], d["w"]
+    if large:  # products far beyond fp16's 65504, weights that bring their sums back
+        s = (s.astype(np.float32) * 2.0 ** 17 / 8).astype(np.float16)
+        w = (w * 2.0 ** -12).astype(np.float32)
+    A = (d["A"] * (64 if large else 1)).astype(np.float16)
+    Wp = wq.wq_prepack_experts(dev(d["Q"]), dev(s), g)
+    Y = wq.wq_gemm_w4a16_experts_combine(dev(A), Wp, dev(d["idx"]), dev(w), dev(d["offsets"]), dev(d["rows"]), N, g)
+    assert wq.wq_get_device_status() == wq.WQ_OK
+    y, ad = oracle.experts_product(A, d["Q"], s, g, d["idx"], by_pair=True)
+    if large:
+        assert np.nanmax(np.abs(y)) > 4 * 65504
+    ref = oracle.experts_combine(y, d["idx"], w)
+    assert np.abs(ref).max() < 60000
+    err, bound = np.abs(f64(Y) - ref), combine_bound_once(y, ad, d["idx"], w, K)
+    assert np.all(err <= bound), np.nanmax(err / bound)
