@@ -39,6 +39,10 @@ namespace {
 
 constexpr int kLThreads = 28 * 32;
 constexpr int kRowsMax = 128;                      // rows of a tile
+// Rows of a tile are rounded up to this: the pair's MMA (M = 256, weights in tensor memory) takes its N
+// in steps of 32. The places behind a tile's last row hold whatever was there; their sums are not stored.
+constexpr int kRowStep = 32;
+static_assert(kRowStep % 32 == 0 && kRowsMax % kRowStep == 0 && kRowsMax <= 256, "N of the pair's MMA");
 constexpr int kColsL = 128;                        // columns of a tile per CTA
 constexpr int kChunkK = 64;                        // weight rows of a chunk: one 128-byte swizzle span
 constexpr int kHalfRows = kRowsMax / 2;            // rows of a tile that one CTA of the pair holds
@@ -188,7 +192,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
     }
     if (warp == kMmaWarp) tmem_alloc2(&s_tmem, 512);
     expert_table<kLThreads>(a.offsets, a.E, a.pairs, kRowsMax, s_start, s_tiles, s_scratch);
-    rows_per_tile<kLThreads>(a.E, 16, s_start, s_tiles, s_each);
+    rows_per_tile<kLThreads>(a.E, kRowStep, s_start, s_tiles, s_each);
     tc_fence_before();
     __syncthreads();
     cluster_sync();  // the barriers of both CTAs stand
@@ -223,7 +227,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
         int place[kHalfRows / 32];
         int have = 0;       // rows of that tile that this CTA holds
         auto read_rows = [&]() {
-            const int half = t.done() ? 0 : (t.nrows + 15) / 16 * 8, first = rank * half;
+            const int half = t.done() ? 0 : (t.nrows + kRowStep - 1) / kRowStep * (kRowStep / 2), first = rank * half;
             have = t.done() ? 0 : max(0, min(half, t.nrows - first));
 #pragma unroll
             for (int j = 0; j < kHalfRows / 32; ++j)
@@ -304,7 +308,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
                     if (ok && !ready) ok = wait_phase(&bars.full[stage], ph, ctl);
                     if (!ok) break;
                     tc_fence_after();
-                    if (kb == 0) idesc = idesc_f16_f32(2 * kColsL, (*(volatile int*)&s_rows_of[stage] + 15) / 16 * 16);
+                    if (kb == 0)
+                        idesc = idesc_f16_f32(2 * kColsL,
+                                              (*(volatile int*)&s_rows_of[stage] + kRowStep - 1) / kRowStep * kRowStep);
                     const uint64_t db = smem_desc_advance(desc0, stage * kStageBytes);
                     const uint32_t wa = tmem + kTmemA + (stage % kSlotsA) * kChunkK;
                     constexpr int kGroups = SL < 2 ? 1 : SL;  // groups of a k-block

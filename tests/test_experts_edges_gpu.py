@@ -9,7 +9,7 @@ pytestmark = [pytest.mark.gpu,
 
 import bit_weight_quantized_prepack_b200 as wq  # noqa: E402
 import oracle  # noqa: E402
-from experts_check import combine_bound_once, experts_inputs  # noqa: E402
+from experts_check import combine_bound_once, experts_inputs, gated_bound, product_bound  # noqa: E402
 
 
 def dev(x):
@@ -45,3 +45,26 @@ def test_combine_rounds_once(E, K, N, g, T, k, padded, large):
     assert np.abs(ref).max() < 60000
     err, bound = np.abs(f64(Y) - ref), combine_bound_once(y, ad, d["idx"], w, K)
     assert np.all(err <= bound), np.nanmax(err / bound)
+
+
+# ------------------------------------------------------------------ every count of rows of a tile
+@pytest.mark.parametrize("K,N,g", [(256, 272, 128), (384, 272, 384), (128, 304, 64), (128, 272, 32)])
+def test_every_row_count_of_an_expert(K, N, g):
+    # n of 200 tokens take expert 0, the others expert 1: many rows an expert on average
+    E, T = 2, 200
+    d = experts_inputs(E, K, N, g, T, 1, seed=K + g)
+    Wp = wq.wq_prepack_experts(dev(d["Q"]), dev(d["s"]), g)
+    Wg = wq.wq_prepack_experts(dev(d["Q"]), dev(d["s"]), g, gated=True)
+    A = dev(d["A"])
+    per = [oracle.experts_product(d["A"], d["Q"], d["s"], g, np.full((T, 1), e)) for e in range(E)]
+    rng = np.random.default_rng(0)
+    for n in range(1, 129):
+        idx = np.ones((T, 1), dtype=np.int32)
+        idx[rng.permutation(T)[:n]] = 0
+        offsets, rows = wq.wq_expert_lists(dev(idx), E)
+        y, ad = (np.where(idx == 0, per[0][i], per[1][i]) for i in (0, 1))
+        for gated, wp, ref, bound in ((False, Wp, y, product_bound(y, ad, K)),
+                                      (True, Wg, oracle.experts_gated(y), gated_bound(y, ad, K))):
+            got = f64(wq.wq_gemm_w4a16_experts(A, wp, offsets, rows, N, g, gated=gated))
+            assert np.all(np.abs(got - ref) <= bound), (n, gated)
+    assert wq.wq_get_device_status() == wq.WQ_OK
