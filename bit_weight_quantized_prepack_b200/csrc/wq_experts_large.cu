@@ -343,9 +343,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
                     ready = mbar_test_wait(&bars.full[stage], ph);
                 }
             }
-            // every MMA done before the CTA frees its tensor memory
             tc_commit2(&bars.drain);
-            wait_phase(&bars.drain, 0, ctl, false);
         }
         __syncwarp();
     } else if (warp >= kDqWarp0) {
@@ -547,6 +545,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
     }
     tc_fence_before();
     __syncthreads();
+    // Both CTAs wait for every commit that nobody has waited for yet: the last k-block's of each stage, and
+    // the drain, which a leader that gave up sends too. No MMA may run on freed tensor memory and no
+    // arrival reach a CTA that has left. Only now, with the CTA's roles at their end: the limit is on
+    // a wait, not on a call.
+    if (warp == kMmaWarp) {
+        const unsigned pairs = gridDim.x / 2;
+        const long long tiles = static_cast<long long>(s_tiles[a.E]) * ((a.N + 2 * kColsL - 1) / (2 * kColsL));
+        const unsigned blocks = static_cast<unsigned>((tiles + pairs - 1 - blockIdx.x / 2) / pairs) * (a.K / kTileK);
+        if (lane < kStages && lane < blocks) wait_phase(&bars.empty[lane], ((blocks - lane - 1) / kStages) & 1, ctl);
+        if (lane == kStages) wait_phase(&bars.drain, 0, ctl, false);
+        __syncwarp();
+    }
     cluster_sync();  // neither CTA leaves, or frees tensor memory, before both are done
     if (warp == kMmaWarp) {
         tc_fence_after();
