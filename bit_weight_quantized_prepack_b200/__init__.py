@@ -626,7 +626,8 @@ def _empty_on(stream, dev):
     if stream is None:
         return torch.empty
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        # handle 0 is the default stream; torch would take an ExternalStream of it from its pool
+        stream = torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) else torch.cuda.default_stream(dev)
 
     def empty(*shape, **kw):
         with torch.cuda.stream(stream):

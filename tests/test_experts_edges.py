@@ -2,6 +2,7 @@
 import ctypes
 
 import pytest
+import torch
 
 import bit_weight_quantized_prepack_b200 as wq
 
@@ -12,3 +13,29 @@ def test_scratch_holds_the_pairs_unrounded(T, E, k, N):
     ok = ctypes.c_void_p(0x10000)  # never dereferenced: the call ends before a launch
     assert wq.lib.wq_gemm_w4a16_experts_combine(ok, ok, ok, ok, ok, ok, ok, ok, T * k * N * 4 - 1, T, E, k, N, 128, 128,
                                                 None) == wq.WQ_ERR_INVALID_ARG
+
+
+# ------------------------------------------------------------------ the stream whose memory outputs are
+@pytest.mark.parametrize("stream,want", [(0, "default"), (4711, "external 4711")])
+def test_outputs_belong_to_the_stream_of_the_handle(monkeypatch, stream, want):
+    entered = []
+
+    class Entered:
+        def __init__(self, s):
+            entered.append(s)
+
+        def __enter__(self):
+            return self
+
+        def __exit__(self, *a):
+            return False
+
+    class External:
+        def __new__(cls, handle, device=None):
+            assert handle != 0, "torch would make a new stream for handle 0"
+            return f"external {handle}"
+    monkeypatch.setattr(torch.cuda, "ExternalStream", External)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: "default")
+    monkeypatch.setattr(torch.cuda, "stream", Entered)
+    t = wq._empty_on(stream, torch.device("cpu"))(3, dtype=torch.float16, device="cpu")
+    assert t.shape == (3,) and entered == [want]

@@ -68,3 +68,31 @@ def test_every_row_count_of_an_expert(K, N, g):
             got = f64(wq.wq_gemm_w4a16_experts(A, wp, offsets, rows, N, g, gated=gated))
             assert np.all(np.abs(got - ref) <= bound), (n, gated)
     assert wq.wq_get_device_status() == wq.WQ_OK
+
+
+# ------------------------------------------------------------------ the default stream by its handle
+def test_the_default_stream_by_its_handle():
+    # what a call on stream 0 returned and the caller dropped goes to later work of the default stream only
+    x = torch.randn((4096, 256), device="cuda")
+    side = [torch.cuda.Stream() for _ in range(40)]  # more than torch keeps of them: all are in here
+    for handle in (0, torch.cuda.default_stream().cuda_stream):
+        want = wq.wq_route_experts(x, 8, lists=True)
+        torch.cuda.synchronize()
+        out = wq.wq_route_experts(x, 8, lists=True, stream=handle)
+        held = {t.data_ptr() for t in out}
+        shapes = [(t.shape, t.dtype) for t in out]
+        del out
+        for s in side:
+            with torch.cuda.stream(s):
+                assert not held & {torch.empty(shape, dtype=dtype, device="cuda").fill_(-3).data_ptr()
+                                   for shape, dtype in shapes}
+        assert held & {torch.empty(shape, dtype=dtype, device="cuda").data_ptr() for shape, dtype in shapes}
+        outs = []
+        for i in range(20):
+            outs.append(wq.wq_route_experts(x, 8, lists=True, stream=handle))
+            with torch.cuda.stream(side[i]):
+                for shape, dtype in shapes:
+                    torch.empty(shape, dtype=dtype, device="cuda").fill_(-3)
+        torch.cuda.synchronize()
+        for got in outs:
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
