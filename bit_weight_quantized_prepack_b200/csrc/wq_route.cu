@@ -77,9 +77,10 @@ __device__ __forceinline__ void warp_best(unsigned key, int index, unsigned* bes
     *best_index = static_cast<int>(__reduce_min_sync(kFull, key == *best ? static_cast<unsigned>(index) : kFull));
 }
 
-// Whether two values of c in 32 bits may stand in the other order.
+// Whether two values of c in 32 bits may stand in the other order. Also where both passed the range of 32 bits
+// (sums of two biases near the type's lowest value): their difference is no number.
 __device__ __forceinline__ bool too_close(float hi, float lo, float terms, float err) {
-    return hi - lo <= 2.0f * terms * err + (fabsf(hi) + fabsf(lo)) * terms * kRoundErr;
+    return !(hi - lo > 2.0f * terms * err + (fabsf(hi) + fabsf(lo)) * terms * kRoundErr);
 }
 
 __device__ __forceinline__ float logit(const RouteArgs& a, int t, int e) {

@@ -95,3 +95,29 @@ def test_the_default_stream_by_its_handle():
         torch.cuda.synchronize()
         for got in outs:
             assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ------------------------------------------------------------------ routing
+def _check_route(x, k, bias=None, **kw):
+    idx_ref, w_ref = oracle.route_experts(x.double().cpu().numpy(), k, bias=None if bias is None else f64(bias), **kw)
+    idx, w, offsets, rows = wq.wq_route_experts(x, k, bias=bias, lists=True, **kw)
+    assert np.array_equal(idx.cpu().numpy(), idx_ref)
+    # fp32: half a step, and the 64-bit score's own error far below it
+    assert np.all(np.abs(f64(w) - w_ref) <= 2.0 ** -24 * np.abs(w_ref) * 1.001 + 2.0 ** -149)
+    o_ref, r_ref = oracle.expert_lists(idx_ref, x.shape[1])
+    assert np.array_equal(offsets.cpu().numpy(), o_ref)
+    assert np.array_equal(rows.cpu().numpy()[:r_ref.size], r_ref)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("sign", [-1, 1])
+@pytest.mark.parametrize("E", [32, 320])
+def test_route_groups_whose_sums_pass_the_range_of_32_bits(score, sign, E):
+    # biases of the type's lowest (largest) value: sums of two of them are told apart in 64 bits
+    top = float(np.finfo(np.float32).max)
+    b = torch.full((4, E // 4), -top)
+    b[0, :], b[1, 2:4], b[2, 1], b[2, 5], b[3, 6:8] = -top, -2.0e38, -2.4e38, -2.6e38, 0.5
+    b = (sign * b).reshape(-1).cuda()
+    x = torch.randn((40, E), generator=torch.Generator().manual_seed(E)).cuda()
+    for top_groups in (1, 2, 3):
+        _check_route(x, 5, b, score=score, groups=4, top_groups=top_groups, group_top=2)
