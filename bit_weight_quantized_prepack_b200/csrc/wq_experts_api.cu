@@ -21,8 +21,10 @@ int status_of(cudaError_t e) {
     return WQ_ERR_CUDA;
 }
 
+// top_k may pass E here: of the experts that a token takes only some may be this device's. Only the
+// routing, which chooses among E, wants top_k <= E.
 int check_counts(int T, int E, int top_k) {
-    if (T < 0 || E <= 0 || top_k <= 0 || top_k > E) return WQ_ERR_INVALID_ARG;
+    if (T < 0 || E <= 0 || top_k <= 0) return WQ_ERR_INVALID_ARG;
     if (E > kExMaxExperts || top_k > kExMaxTopK || T > kMaxTokens || static_cast<long long>(T) * top_k > kMaxPairs)
         return WQ_ERR_UNSUPPORTED_SHAPE;
     return WQ_OK;
@@ -71,6 +73,7 @@ extern "C" {
 int wq_route_experts(const void* logits, int logits_fp32, const float* bias, int T, int E, int top_k, int score,
                      int groups, int top_groups, int group_top, int renorm, float scale, int32_t* idx, float* w,
                      int32_t* offsets, int32_t* rows, void* stream) {
+    if (E > 0 && top_k > E) return WQ_ERR_INVALID_ARG;
     int rc = check_counts(T, E, top_k);
     if (rc) return rc;
     if (logits_fp32 < 0 || logits_fp32 > 1 || score < 0 || score > 1 || renorm < 0 || renorm > 1 || group_top < 1 ||

@@ -39,3 +39,19 @@ def test_outputs_belong_to_the_stream_of_the_handle(monkeypatch, stream, want):
     monkeypatch.setattr(torch.cuda, "stream", Entered)
     t = wq._empty_on(stream, torch.device("cpu"))(3, dtype=torch.float16, device="cpu")
     assert t.shape == (3,) and entered == [want]
+
+
+# ------------------------------------------------------------------ more choices than experts of this device
+def test_lists_and_products_take_more_choices_than_experts():
+    L, P = wq.lib, ctypes.c_void_p
+    ok, odd = P(0x10000), P(0x10002)  # never dereferenced: the misaligned pointer ends every call before a launch
+    T, E, k, N, K, g = 5, 4, 8, 32, 128, 128
+    assert wq.wq_experts_scratch_bytes(T, E, k, N) == T * k * N * 4
+    assert L.wq_expert_lists(ok, T, E, k, ok, odd, None) == wq.WQ_ERR_MISALIGNED
+    assert L.wq_gemm_w4a16_experts(ok, ok, ok, odd, ok, T, E, k, N, K, g, 0, None) == wq.WQ_ERR_MISALIGNED
+    assert L.wq_gemm_w4a16_experts_combine(ok, ok, ok, odd, ok, ok, ok, ok, 1 << 20, T, E, k, N, K, g,
+                                           None) == wq.WQ_ERR_MISALIGNED
+    # 32 choices at most, and the routing chooses among E
+    assert L.wq_expert_lists(ok, T, E, 33, ok, odd, None) == wq.WQ_ERR_UNSUPPORTED_SHAPE
+    assert L.wq_route_experts(ok, 1, None, T, E, k, 0, 1, 1, 1, 1, 1.0, ok, ok, None, None,
+                              None) == wq.WQ_ERR_INVALID_ARG

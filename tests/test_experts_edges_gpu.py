@@ -121,3 +121,32 @@ def test_route_groups_whose_sums_pass_the_range_of_32_bits(score, sign, E):
     x = torch.randn((40, E), generator=torch.Generator().manual_seed(E)).cuda()
     for top_groups in (1, 2, 3):
         _check_route(x, 5, b, score=score, groups=4, top_groups=top_groups, group_top=2)
+
+
+# ------------------------------------------------------------------ some of the experts of a layer
+@pytest.mark.parametrize("T", [1, 9, 300, 2500])
+@pytest.mark.parametrize("E", [1, 4])
+def test_more_choices_than_experts_here(T, E):
+    # 8 of 32 experts a token, E of them on this device
+    K, N, g, k = 256, 80, 128, 8
+    d = experts_inputs(32, K, N, g, T, k, seed=T + E, by_pair=True)
+    idx = d["idx"] - 8
+    Q, s = d["Q"][8:8 + E], d["s"][8:8 + E]
+    Wp = wq.wq_prepack_experts(dev(Q), dev(s), g)
+    offsets, rows = wq.wq_expert_lists(dev(idx), E)
+    here = (idx >= 0) & (idx < E)
+    o_ref, r_ref = oracle.expert_lists(np.where(here, idx, -1), E)
+    assert np.array_equal(offsets.cpu().numpy(), o_ref) and np.array_equal(rows.cpu().numpy()[:r_ref.size], r_ref)
+    seen = np.where(here, idx, -1)
+    A = d["A"][:T]
+    Y = torch.full((T * k, N), -77.0, dtype=torch.float16, device="cuda")
+    wq.wq_gemm_w4a16_experts(dev(A), Wp, offsets, rows, N, g, Y=Y)
+    y, ad = oracle.experts_product(A, Q, s, g, seen)
+    listed = here.reshape(-1)
+    assert np.all(f64(Y)[~listed] == -77.0)
+    assert np.all(np.abs(f64(Y) - y)[listed] <= product_bound(y, ad, K)[listed])
+    out = wq.wq_gemm_w4a16_experts_combine(dev(d["A"]), Wp, dev(idx), dev(d["w"]), offsets, rows, N, g)
+    y, ad = oracle.experts_product(d["A"], Q, s, g, seen, by_pair=True)
+    ref = oracle.experts_combine(y, seen, d["w"])
+    assert np.all(np.abs(f64(out) - ref) <= combine_bound_once(y, ad, seen, d["w"], K))
+    assert wq.wq_get_device_status() == wq.WQ_OK
