@@ -85,7 +85,7 @@ def _load():
         "wq_prepack_mixed": (I, [P, P, P, I, I, I, P, Z, P]),
         "wq_unpack_mixed": (I, [P, I, I, I, P, P, P, P]),
         "wq_gemm_w4a16_mixed": (I, [P, P, Z, P, I, I, I, I, P]),
-        "wq_route_experts": (I, [P, I, P, I, I, I, I, I, I, I, I, ctypes.c_float, P, P, P, P, P]),
+        "wq_route_experts": (I, [P, I, P, I, I, I, I, I, I, I, I, ctypes.c_double, P, P, P, P, P]),
         "wq_expert_lists": (I, [P, I, I, I, P, P, P]),
         "wq_prepacked_bytes_experts": (Z, [I, I, I, I]),
         "wq_prepack_experts": (I, [P, P, I, I, I, I, I, P, P]),

@@ -63,7 +63,7 @@ struct RouteArgs {
     int sigmoid;
     int groups, top_groups, group_top;
     int renorm;
-    float scale;
+    double scale;
 };
 
 struct ExpertArgs {

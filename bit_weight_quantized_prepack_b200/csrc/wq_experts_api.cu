@@ -71,7 +71,7 @@ ExpertArgs product_args(const uint16_t* A, const void* Wp, const int32_t* offset
 extern "C" {
 
 int wq_route_experts(const void* logits, int logits_fp32, const float* bias, int T, int E, int top_k, int score,
-                     int groups, int top_groups, int group_top, int renorm, float scale, int32_t* idx, float* w,
+                     int groups, int top_groups, int group_top, int renorm, double scale, int32_t* idx, float* w,
                      int32_t* offsets, int32_t* rows, void* stream) {
     if (E > 0 && top_k > E) return WQ_ERR_INVALID_ARG;
     int rc = check_counts(T, E, top_k);

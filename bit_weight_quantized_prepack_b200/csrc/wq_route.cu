@@ -483,7 +483,7 @@ __device__ __forceinline__ int route_token(const RouteArgs& a, int t, double* sc
     if (lane < a.top_k) {
         const size_t at = static_cast<size_t>(t) * a.top_k + lane;
         a.idx[at] = mine;
-        a.w[at] = static_cast<float>(p * static_cast<double>(a.scale));
+        a.w[at] = static_cast<float>(p * a.scale);
     }
     return mine;
 }

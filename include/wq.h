@@ -331,7 +331,7 @@ WQ_API int wq_gemm_w4a16_noalloc(const uint16_t* A, const void* Wp, uint16_t* Y,
  * write until it has completed (0 for few pairs, T * top_k <= E / 4: it may then be null). Y and
  * scratch must overlap neither each other nor an input. */
 WQ_API int wq_route_experts(const void* logits, int logits_fp32, const float* bias, int T, int E, int top_k, int score,
-                 int groups, int top_groups, int group_top, int renorm, float scale, int32_t* idx, float* w,
+                 int groups, int top_groups, int group_top, int renorm, double scale, int32_t* idx, float* w,
                  int32_t* offsets, int32_t* rows, void* stream);
 WQ_API int wq_expert_lists(const int32_t* idx, int T, int E, int top_k, int32_t* offsets, int32_t* rows, void* stream);
 WQ_API size_t wq_prepacked_bytes_experts(int E, int K, int N, int g);

@@ -1,5 +1,7 @@
 """CPU tests of the expert operators at their edges: sizes, counts and refusals."""
 import ctypes
+import os
+import re
 
 import pytest
 import torch
@@ -55,3 +57,14 @@ def test_lists_and_products_take_more_choices_than_experts():
     assert L.wq_expert_lists(ok, T, E, 33, ok, odd, None) == wq.WQ_ERR_UNSUPPORTED_SHAPE
     assert L.wq_route_experts(ok, 1, None, T, E, k, 0, 1, 1, 1, 1, 1.0, ok, ok, None, None,
                               None) == wq.WQ_ERR_INVALID_ARG
+
+
+# ------------------------------------------------------------------ the factor of the weights
+def test_the_scale_reaches_the_library_in_64_bits():
+    # the weights are computed in 64 bits and rounded once, so their factor must not be rounded before
+    at = [i for i, t in enumerate(wq.lib.wq_route_experts.argtypes) if t in (ctypes.c_float, ctypes.c_double)]
+    assert len(at) == 1 and wq.lib.wq_route_experts.argtypes[at[0]] is ctypes.c_double
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "include", "wq.h")).read()
+    args = re.search(r"WQ_API int wq_route_experts\((.*?)\);", text, re.S).group(1).split(",")
+    assert args[at[0]].split() == ["double", "scale"]

@@ -150,3 +150,12 @@ def test_more_choices_than_experts_here(T, E):
     ref = oracle.experts_combine(y, seen, d["w"])
     assert np.all(np.abs(f64(out) - ref) <= combine_bound_once(y, ad, seen, d["w"], K))
     assert wq.wq_get_device_status() == wq.WQ_OK
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_with_a_scale_that_32_bits_do_not_hold(score, renorm):
+    # 2.446 is off by 2^-25 of itself in fp32: half of a weight's own rounding again
+    x = torch.randn((500, 64), generator=torch.Generator().manual_seed(1)).cuda()
+    for scale in (2.446, 0.1, 16.0 / 3):
+        _check_route(x, 6, score=score, renorm=renorm, scale=scale)
