@@ -37,10 +37,11 @@ constexpr int kListThreads = 1024, kListExperts = 2;
 constexpr int kNotes = 64;   // choices a thread notes at a time
 // What c in 32 bits may be off. __expf is within 2 + 1.173 |x| units in the last place. Sigmoid: that
 // error times p (1 - p), below 0.6 * 2^-23, the rounding of 1 + e and the rounded reciprocal: below
-// 2e-7. Softmax: p off by the same of its own term, below 2^-22, and by the sum's share, below p
-// times 2^-23 (2 + 1.7 ln E) + 37 * 2^-24 for up to 1024 terms: below 4e-6. The sum with the bias, and
-// of two such, is rounded: 2^-23 of the magnitude covers one rounding twice over.
-constexpr float kSigmoidErr = 2.5e-7f, kSoftmaxErr = 4.0e-6f, kRoundErr = 1.2e-7f;
+// 2e-7. Softmax: p off by the same of its own term, below 2^-22 = 2.4e-7; by the sum's share, below p
+// times 2^-23 (2 + 1.7 ln E) + 37 * 2^-24, for up to 1024 terms 1.65e-6 + 2.21e-6; by the quotient's 2
+// units and the product's rounding, p times 2^-22 + 2^-24 = 3.0e-7: below 4.5e-6 together. The sum with
+// the bias, and of two such, is rounded: 2^-23 of the magnitude covers one rounding twice over.
+constexpr float kSigmoidErr = 2.5e-7f, kSoftmaxErr = 4.5e-6f, kRoundErr = 1.2e-7f;
 
 __device__ __forceinline__ unsigned long long key_of(double v) {
     const unsigned long long b = static_cast<unsigned long long>(__double_as_longlong(v + 0.0));  // -0 -> +0

@@ -1,5 +1,6 @@
 """CPU tests of the expert operators at their edges: sizes, counts and refusals."""
 import ctypes
+import math
 import os
 import re
 
@@ -68,3 +69,15 @@ def test_the_scale_reaches_the_library_in_64_bits():
     text = open(os.path.join(root, "include", "wq.h")).read()
     args = re.search(r"WQ_API int wq_route_experts\((.*?)\);", text, re.S).group(1).split(",")
     assert args[at[0]].split() == ["double", "scale"]
+
+
+def test_the_bound_of_32_bit_scores_covers_its_terms():
+    # terms of the softmax bound as the kernel's comment derives them, at the largest E
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "bit_weight_quantized_prepack_b200", "csrc", "wq_route.cu")).read()
+    err = float(re.search(r"kSoftmaxErr = ([0-9.e-]+)f", text).group(1))
+    E = 1024
+    own = 2.0 ** -22
+    total = 2.0 ** -23 * (2 + 1.7 * math.log(E)) + 37 * 2.0 ** -24
+    quotient = 2.0 ** -22 + 2.0 ** -24
+    assert own + total + quotient <= err

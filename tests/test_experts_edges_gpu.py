@@ -155,7 +155,7 @@ def test_more_choices_than_experts_here(T, E):
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [False, True])
 def test_route_with_a_scale_that_32_bits_do_not_hold(score, renorm):
-    # 2.446 is off by 2^-25 of itself in fp32: half of a weight's own rounding again
+    # 2.446 is off by 0.68 * 2^-24 of itself in fp32: more than half of a weight's own rounding again
     x = torch.randn((500, 64), generator=torch.Generator().manual_seed(1)).cuda()
     for scale in (2.446, 0.1, 16.0 / 3):
         _check_route(x, 6, score=score, renorm=renorm, scale=scale)
