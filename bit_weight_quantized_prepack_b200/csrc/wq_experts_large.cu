@@ -73,15 +73,49 @@ struct Ctl {
     unsigned long long timeout_ns;
 };
 
-// Arrive on the leader's barrier that lies where `bar` lies in this CTA. What the leader's MMAs
-// read is ordered by the proxy and tcgen05 fences before it, not by this arrival: one that releases
-// at cluster scope costs its thread some hundred cycles (4096 tokens, 128 experts of 2048 x 1536: 366 us against 221).
+// Arrive on the leader's barrier that lies where `bar` lies in this CTA, for what lies in tensor memory:
+// weights stored there, sums read from there. Those are ordered by the tcgen05 fences of both sides around
+// the barrier, which want no more of it than that one thread's step comes after the other's; nothing
+// else is handed over with these arrivals. (Released at cluster scope all the same, they cost their
+// threads some hundred cycles each: 4096 tokens, 128 experts of 2048 x 1536, 334 us with the weights', 447
+// with the sums' too, against 284.)
 __device__ __forceinline__ void mbar_arrive_leader(uint64_t* bar) {
     asm volatile(
         "{\n\t.reg .b32 remote;\n\t"
         "mapa.shared::cluster.u32 remote, %0, 0;\n\t"
         "mbarrier.arrive.shared::cluster.b64 _, [remote];\n\t}" ::"r"(smem_addr(bar))
         : "memory");
+}
+// The same for rows in shared memory: what this thread wrote, or has seen written, is released at cluster
+// scope to the leader's thread, whose wait acquires it there (2 us of 282).
+__device__ __forceinline__ void mbar_arrive_leader_release(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .b32 remote;\n\t"
+        "mapa.shared::cluster.u32 remote, %0, 0;\n\t"
+        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [remote];\n\t}" ::"r"(smem_addr(bar))
+        : "memory");
+}
+__device__ __forceinline__ bool mbar_test_wait_cluster(uint64_t* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+__device__ __forceinline__ bool mbar_try_wait_sleep_cluster(uint64_t* bar, uint32_t parity, uint32_t suspend_ns) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(suspend_ns)
+        : "memory");
+    return done != 0;
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -92,13 +126,18 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     return r;
 }
 
-// Bounded wait for a phase; false when it expired or another role gave up.
+// Bounded wait for a phase; false when it expired or another role gave up. kCluster: what the arrivals of
+// both CTAs released is acquired.
+template <bool kCluster = false>
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, const Ctl& c, bool honour_stop = true) {
-    if (mbar_test_wait(bar, parity)) return true;
-    if (mbar_try_wait_sleep(bar, parity, 20000)) return true;  // the timer is read only by long waits
+    const auto tried = [&] {
+        return kCluster ? mbar_try_wait_sleep_cluster(bar, parity, 20000) : mbar_try_wait_sleep(bar, parity, 20000);
+    };
+    if (kCluster ? mbar_test_wait_cluster(bar, parity) : mbar_test_wait(bar, parity)) return true;
+    if (tried()) return true;  // the timer is read only by long waits
     const uint64_t t0 = global_timer_ns();
     while (true) {
-        if (mbar_try_wait_sleep(bar, parity, 20000)) return true;
+        if (tried()) return true;
         if (honour_stop && *c.stop) return false;
         if (global_timer_ns() - t0 > c.timeout_ns) {
             *c.stop = 1;
@@ -220,7 +259,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
         auto signal = [&]() {
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive_leader(&bars.full[last]);
+            if (lane == 0) mbar_arrive_leader_release(&bars.full[last]);
         };
         // Entries of the lists of the next tile, read while this one is copied: lane l the rows l, l +
         // 32, .. of this CTA's half; places behind its last row repeat that row.
@@ -299,13 +338,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
             unsigned m = 0;  // groups so far: sums m & 1
             bool ok = true;
             const uint64_t desc0 = smem_desc_sw128(smem_addr(ring));
-            bool ready = mbar_test_wait(&bars.full[0], 0);
+            bool ready = mbar_test_wait_cluster(&bars.full[0], 0);
             for (int left = t.left(gridDim.x / 2); ok && left > 0; --left) {
                 uint32_t idesc = 0;
                 int in_group = 0;  // k-blocks of the group that have been issued
                 for (int kb = 0; kb < KT; ++kb) {
                     if (SL < 2 && in_group == 0) ok = wait_phase(&bars.sum_empty[m & 1], ((m >> 1) & 1) ^ 1, ctl);
-                    if (ok && !ready) ok = wait_phase(&bars.full[stage], ph, ctl);
+                    if (ok && !ready) ok = wait_phase<true>(&bars.full[stage], ph, ctl);
                     if (!ok) break;
                     tc_fence_after();
                     if (kb == 0)
@@ -340,7 +379,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
                     }
                     stage = (stage + 1) % kStages;
                     ph ^= stage == 0;
-                    ready = mbar_test_wait(&bars.full[stage], ph);
+                    ready = mbar_test_wait_cluster(&bars.full[stage], ph);
                 }
             }
             tc_commit2(&bars.drain);

@@ -208,3 +208,15 @@ def test_the_kernel_waits_in_both_ctas():
     tail = src[src.index("cluster_sync();  // neither CTA leaves") - 1400:src.index("cluster_sync();  // neither CTA leaves")]
     tail = tail[tail.index("__syncthreads();"):]
     assert "wait_phase(&bars.drain" in tail and "wait_phase(&bars.empty" in tail and "rank" not in tail
+
+
+def test_rows_are_released_and_acquired_at_cluster_scope():
+    # the rows that one CTA's warps copied are read for the other CTA's thread
+    import os
+    src = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                            "bit_weight_quantized_prepack_b200", "csrc", "wq_experts_large.cu")).read()
+    gather = src[src.index("rows of the activations"):src.index("// ---------------------------------------------------------------- MMAs")]
+    assert "mbar_arrive_leader_release(&bars.full" in gather and "mbar_arrive_leader(" not in gather
+    mma = src[src.index("// ---------------------------------------------------------------- MMAs"):src.index("---- weights")]
+    assert "wait_phase<true>(&bars.full" in mma
+    assert "wait_phase(&bars.full" not in mma and "mbar_test_wait(&bars.full" not in mma
