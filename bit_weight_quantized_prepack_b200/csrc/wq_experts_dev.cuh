@@ -83,6 +83,9 @@ __device__ __forceinline__ int row_of_pair(int p, const ExpertArgs& a) {
     return a.a_div == 1 ? p : r - (r * a.a_div > p);
 }
 
+// silu(gate) * up, off by less than (8 + 1.18 |gate|) 2^-23 of itself: exp's 2 + 1.173 |gate| units in the last
+// place, the quotient's 2, three roundings. At gate = -104, where exp passes the range, that is 2^-16, a
+// thirtieth of the output's rounding; from there on the value is 0 (fp32 itself leaves 2^-147 of up).
 __device__ __forceinline__ float silu_mul(float gate, float up) { return __fdividef(gate, 1.0f + __expf(-gate)) * up; }
 
 // Rows of each of an expert's row tiles: even shares, rounded up to `unit` rows.

@@ -159,3 +159,36 @@ def test_route_with_a_scale_that_32_bits_do_not_hold(score, renorm):
     x = torch.randn((500, 64), generator=torch.Generator().manual_seed(1)).cuda()
     for scale in (2.446, 0.1, 16.0 / 3):
         _check_route(x, 6, score=score, renorm=renorm, scale=scale)
+
+
+# ------------------------------------------------------------------ the gate over its whole range
+@pytest.mark.parametrize("E,T", [(64, 9), (4, 30), (2, 300)])  # few pairs, few rows, many rows
+def test_gated_over_the_whole_range_of_the_gate(E, T):
+    # rows of one 1 make the sums the weights themselves, exact in fp32: gates from -110 to 110, ups to
+    # 59904 so that what a gate of -24 leaves is still above fp16's smallest
+    K, N, g = 128, 64, 128
+    rng = np.random.default_rng(E)
+    q = rng.integers(0, 16, (E, K, N))
+    q[:, :, N // 2:] = rng.choice([0, 1, 15], (E, K, N // 2))
+    Q = np.zeros((E, K // 8, N), dtype=np.uint32)
+    for j in range(8):
+        Q |= q[:, j::8].astype(np.uint32) << np.uint32(4 * j)
+    s = np.empty((E, 1, N), dtype=np.float16)
+    s[:, 0, :N // 2] = 13.75 * 2.0 ** -rng.integers(0, 8, (E, N // 2))
+    s[:, 0, N // 2:] = 7486.0 * 2.0 ** -rng.integers(0, 10, (E, N // 2))
+    A = np.zeros((T, K), dtype=np.float16)
+    A[np.arange(T), rng.integers(0, K, T)] = 1.0
+    idx = rng.integers(0, E, (T, 1)).astype(np.int32)
+    Wp = wq.wq_prepack_experts(dev(Q.view(np.int32)), dev(s), g, gated=True)
+    offsets, rows = wq.wq_expert_lists(dev(idx), E)
+    got = f64(wq.wq_gemm_w4a16_experts(dev(A), Wp, offsets, rows, N, g, gated=True))
+    y, _ = oracle.experts_product(A, Q.view(np.int32), s, g, idx)
+    gate = y[:, :N // 2]
+    assert gate.min() < -100 and gate.max() > 90
+    ref = oracle.experts_gated(y)
+    # fp32's quotient and product of such ups may also pass below the normal range: 2^-100 covers it
+    rel = (8 + 1.18 * np.abs(gate)) * 2.0 ** -23
+    over = np.abs(ref) * (1 + 2.0 ** -10) >= 65504
+    bound = rel * np.abs(ref) + np.maximum(2.0 ** -11 * np.abs(ref) * (1 + 2.0 ** -10), 2.0 ** -25) + 2.0 ** -100
+    assert np.all(np.abs(got - ref)[~over] <= bound[~over])
+    assert np.all(np.abs(got[over]) >= 65400) and np.all(np.sign(got[over]) == np.sign(ref[over]))
