@@ -81,3 +81,14 @@ def test_the_bound_of_32_bit_scores_covers_its_terms():
     total = 2.0 ** -23 * (2 + 1.7 * math.log(E)) + 37 * 2.0 ** -24
     quotient = 2.0 ** -22 + 2.0 ** -24
     assert own + total + quotient <= err
+
+
+# ------------------------------------------------------------------ the C ABI
+def test_header_and_library_have_the_expert_entry_points():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    declared = re.findall(r"^WQ_API\s+[\w\s\*]+?\b(wq_\w+)\s*\(", open(os.path.join(root, "include", "wq.h")).read(), flags=re.M)
+    raw = ctypes.CDLL(wq.LIB_PATH)
+    for name in ("wq_route_experts", "wq_expert_lists", "wq_prepacked_bytes_experts", "wq_prepack_experts",
+                 "wq_unpack_experts", "wq_gemm_w4a16_experts", "wq_experts_scratch_bytes",
+                 "wq_gemm_w4a16_experts_combine"):
+        assert name in declared and hasattr(raw, name) and name in wq.__all__

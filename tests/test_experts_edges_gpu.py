@@ -192,3 +192,94 @@ def test_gated_over_the_whole_range_of_the_gate(E, T):
     bound = rel * np.abs(ref) + np.maximum(2.0 ** -11 * np.abs(ref) * (1 + 2.0 ** -10), 2.0 ** -25) + 2.0 ** -100
     assert np.all(np.abs(got - ref)[~over] <= bound[~over])
     assert np.all(np.abs(got[over]) >= 65400) and np.all(np.sign(got[over]) == np.sign(ref[over]))
+
+
+# ------------------------------------------------------------------ sizes on both sides of each switch of kernel
+@pytest.mark.parametrize("K", [4992, 5120, 9984, 10112, 11136, 11264])
+@pytest.mark.parametrize("g", [128, 0])
+def test_the_longest_rows_of_each_form(K, g):
+    # 3 experts, 12 pairs: 8-row tiles with two places for the rows (K up to 4992), one (9984 with 24 warps, 11136
+    # with 16), none (the many-rows kernel)
+    g = g or K
+    E, N, T, k = 3, 72, 6, 2
+    d = experts_inputs(E, K, N, g, T, k, seed=K, by_pair=True)
+    Wp = wq.wq_prepack_experts(dev(d["Q"]), dev(d["s"]), g)
+    lists = dev(d["offsets"]), dev(d["rows"])
+    got = f64(wq.wq_gemm_w4a16_experts(dev(d["A"][:T]), Wp, *lists, N, g))
+    y, ad = oracle.experts_product(d["A"][:T], d["Q"], d["s"], g, d["idx"])
+    assert np.all(np.abs(got - y) <= product_bound(y, ad, K))
+    out = f64(wq.wq_gemm_w4a16_experts_combine(dev(d["A"]), Wp, dev(d["idx"]), dev(d["w"]), *lists, N, g))
+    y, ad = oracle.experts_product(d["A"], d["Q"], d["s"], g, d["idx"], by_pair=True)
+    assert np.all(np.abs(out - oracle.experts_combine(y, d["idx"], d["w"])) <= combine_bound_once(y, ad, d["idx"], d["w"], K))
+    assert wq.wq_get_device_status() == wq.WQ_OK
+
+
+# ------------------------------------------------------------------ offsets beyond 2^31 elements
+def _weights_on_the_device(E, K, N, g, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    Q = torch.randint(-2 ** 31, 2 ** 31, (E, K // 8, N), generator=gen, device="cuda", dtype=torch.int64).to(torch.int32)
+    s = ((0.5 + torch.rand((E, K // g, N), generator=gen, device="cuda")) * (0.22 / K ** 0.5)).to(torch.float16)
+    return Q, s
+
+
+def _some(T):
+    """Tokens at both ends and around the middle."""
+    return [0, 1, T // 2 - 1, T // 2, T - 2, T - 1]
+
+
+@pytest.mark.parametrize("E,K,N,g,T,k", [
+    (2, 128, 16400, 128, 65552, 2),     # many rows: outputs and scratch of 2^31 elements and more
+    (2, 16512, 64, 128, 65052, 2),      # many rows: the pairs' activations
+    (1024, 128, 150000, 64, 7168, 2)])  # few rows: outputs, and 9.8 GB of weights
+def test_offsets_beyond_32_bits(E, K, N, g, T, k):
+    assert max(T * k * N, T * k * K) > 2 ** 31
+    Q, s = _weights_on_the_device(E, K, N, g, seed=N)
+    Wp = wq.wq_prepack_experts(Q, s, g)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    H = torch.randn((T * k, K), generator=gen, device="cuda", dtype=torch.float16)
+    idx = torch.rand((T, E), generator=gen, device="cuda").argsort(1)[:, :k].to(torch.int32).contiguous()
+    w = torch.rand((T, k), generator=gen, device="cuda") + 0.05
+    lists = wq.wq_expert_lists(idx, E)
+    up = wq.wq_gemm_w4a16_experts(H[:T], Wp, *lists, N, g)
+    picked = _some(T)
+    pi = idx[picked].cpu().numpy()
+    used = sorted(set(pi.reshape(-1).tolist()))
+    where = np.vectorize(used.index)(pi)
+    q_, s_ = Q[used].cpu().numpy(), s[used].cpu().numpy()
+    got = f64(up.view(T, k, N)[picked]).reshape(-1, N)
+    y, ad = oracle.experts_product(H[picked].cpu().numpy(), q_, s_, g, where)
+    assert np.all(np.abs(got - y) <= product_bound(y, ad, K))
+    del up
+    out = wq.wq_gemm_w4a16_experts_combine(H, Wp, idx, w, *lists, N, g)
+    h = H.view(T, k, K)[picked].reshape(-1, K).cpu().numpy()
+    y, ad = oracle.experts_product(h, q_, s_, g, where, by_pair=True)
+    wn = w[picked].cpu().numpy()
+    assert np.all(np.abs(f64(out[picked]) - oracle.experts_combine(y, where, wn)) <= combine_bound_once(y, ad, where, wn, K))
+    assert wq.wq_get_device_status() == wq.WQ_OK
+
+
+# ------------------------------------------------------------------ no memory but what the caller gives
+@pytest.mark.parametrize("T", [1, 24, 500])
+def test_calls_with_given_outputs_leave_the_free_memory(T):
+    E, K, N, g, k = 8, 256, 256, 128, 2
+    d = experts_inputs(E, K, N, g, T, k, seed=T, by_pair=True)
+    Q, s, H = dev(d["Q"]), dev(d["s"]), dev(d["A"])
+    Wp = torch.zeros(wq.wq_prepacked_bytes_experts(E, K, N, g), dtype=torch.uint8, device="cuda")
+    x = torch.randn((T, E), device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    idx, w, offsets, rows = torch.empty((T, k), **i32), torch.empty((T, k), device="cuda"), torch.empty(E + 1, **i32), \
+        torch.empty(T * k, **i32)
+    up = torch.empty((T * k, N), dtype=torch.float16, device="cuda")
+    Y = torch.empty((T, N), dtype=torch.float16, device="cuda")
+    scratch = torch.empty(max(16, wq.wq_experts_scratch_bytes(T, E, k, N)), dtype=torch.uint8, device="cuda")
+    for turn in range(3):
+        torch.cuda.synchronize()
+        before = torch.cuda.mem_get_info()[0], torch.cuda.memory_allocated()
+        wq.wq_prepack_experts(Q, s, g, Wp=Wp)
+        wq.wq_route_experts(x, k, idx=idx, w=w)
+        wq.wq_expert_lists(idx, E, offsets=offsets, rows=rows)
+        wq.wq_gemm_w4a16_experts(H[:T], Wp, offsets, rows, N, g, Y=up)
+        wq.wq_gemm_w4a16_experts_combine(H, Wp, idx, w, offsets, rows, N, g, Y=Y, scratch=scratch)
+        torch.cuda.synchronize()
+        if turn:  # the first calls on a device load the library's device code
+            assert (torch.cuda.mem_get_info()[0], torch.cuda.memory_allocated()) == before
