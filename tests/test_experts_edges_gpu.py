@@ -283,3 +283,81 @@ def test_calls_with_given_outputs_leave_the_free_memory(T):
         torch.cuda.synchronize()
         if turn:  # the first calls on a device load the library's device code
             assert (torch.cuda.mem_get_info()[0], torch.cuda.memory_allocated()) == before
+
+
+# ------------------------------------------------------------------ calls at the limits
+def test_the_most_pairs_that_a_call_takes():
+    # 2^24 tokens, 16 choices: 2^28 pairs
+    E, K, N, g, T, k = 16, 128, 8, 128, 1 << 24, 16
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    logits = torch.randn((T, E), generator=gen, device="cuda", dtype=torch.float16)
+    idx, w, offsets, rows = wq.wq_route_experts(logits, k, lists=True)
+    for t0 in (0, T // 2, T - 64):
+        ref, w_ref = oracle.route_experts(f64(logits[t0:t0 + 64]), k)
+        assert np.array_equal(idx[t0:t0 + 64].cpu().numpy(), ref)
+        assert np.all(np.abs(f64(w[t0:t0 + 64]) - w_ref) <= 2.0 ** -24 * 1.001 * w_ref + 2.0 ** -149)
+    flat = idx.view(-1)
+    for e in range(E):  # every token takes every expert once
+        assert int(offsets[e]) == e * T
+        assert torch.equal(rows[e * T:(e + 1) * T].long(), torch.nonzero(flat == e).view(-1))
+    assert int(offsets[E]) == E * T
+    d = experts_inputs(E, K, N, g, 1, 1, seed=4)
+    A = torch.randn((T, K), generator=gen, device="cuda", dtype=torch.float16)
+    Y = wq.wq_gemm_w4a16_experts(A, wq.wq_prepack_experts(dev(d["Q"]), dev(d["s"]), g), offsets, rows, N, g)
+    assert wq.wq_get_device_status() == wq.WQ_OK
+    for t0 in (0, T // 3, T - 64):
+        y, ad = oracle.experts_product(A[t0:t0 + 64].cpu().numpy(), d["Q"], d["s"], g, idx[t0:t0 + 64].cpu().numpy())
+        assert np.all(np.abs(f64(Y[t0 * k:(t0 + 64) * k]) - y) <= product_bound(y, ad, K))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_in_one_launch_at_its_largest(score):
+    gen = torch.Generator().manual_seed(6)
+    x, b = torch.randn((16, 1024), generator=gen).cuda(), (torch.randn(1024, generator=gen) * 0.1).cuda()
+    _check_route(x, 8, b, score=score, groups=64, top_groups=9, group_top=2)
+    _check_route(x[:4].contiguous(), 32, b, score=score)
+
+
+@pytest.mark.parametrize("E,T", [(64, 3), (4, 9), (3, 200)])  # few pairs, few rows, many rows
+def test_rows_of_padded_places_are_not_read(E, T):
+    K, N, g, k = 384, 80, 128, 3
+    d = experts_inputs(E, K, N, g, T, k, seed=E, by_pair=True)
+    rng = np.random.default_rng(T)
+    idx = np.where(rng.random((T, k)) < 0.4, -1, d["idx"])
+    idx[T - 1] = -1
+    H, w = d["A"].copy(), d["w"].copy()
+    H[idx.reshape(-1) < 0] = np.nan
+    w[idx < 0] = np.nan
+    Wp = wq.wq_prepack_experts(dev(d["Q"]), dev(d["s"]), g)
+    lists = wq.wq_expert_lists(dev(idx), E)
+    out = f64(wq.wq_gemm_w4a16_experts_combine(dev(H), Wp, dev(idx), dev(w), *lists, N, g))
+    y, ad = oracle.experts_product(d["A"], d["Q"], d["s"], g, idx, by_pair=True)
+    assert np.all(np.abs(out - oracle.experts_combine(y, idx, d["w"])) <= combine_bound_once(y, ad, idx, d["w"], K))
+    assert not out[T - 1].any()
+
+
+def test_calls_from_several_threads():
+    import threading
+    E, K, N, g, k = 8, 512, 256, 128, 2
+    work = []
+    for i, T in enumerate((1, 20, 400, 33)):
+        d = experts_inputs(E, K, N, g, T, k, seed=i, by_pair=True)
+        Wp = wq.wq_prepack_experts(dev(d["Q"]), dev(d["s"]), g)
+        x, H = torch.randn((T, E), device="cuda"), dev(d["A"])
+
+        def one(stream=None, x=x, H=H, Wp=Wp):
+            idx, w, *lists = wq.wq_route_experts(x, k, lists=True, stream=stream)
+            return wq.wq_gemm_w4a16_experts_combine(H, Wp, idx, w, *lists, N, g, stream=stream)
+        work.append((one, one(), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    outs = [[] for _ in work]
+    threads = [threading.Thread(target=lambda i=i: outs[i].extend(work[i][0](stream=work[i][2]) for _ in range(30)))
+               for i in range(len(work))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for (_, want, _), got in zip(work, outs):
+        assert len(got) == 30 and all(torch.equal(y, want) for y in got)
+    assert wq.wq_get_device_status() == wq.WQ_OK
