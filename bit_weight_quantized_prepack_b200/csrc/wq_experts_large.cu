@@ -202,8 +202,9 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&v)[16]) {
         : "memory");
 }
 
-// SL: scales per k-block and column (1, 2 or 4); 0: per-column, g == K.
-template <int SL>
+// SL: scales per k-block and column (1, 2 or 4); 0: per-column, g == K. kPairs: the products go to y32,
+// unrounded (not gated).
+template <int SL, bool kPairs>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) experts_large_kernel(LargeArgs args) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ Bars bars;
@@ -532,7 +533,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
                 if (4 * i + part >= pieces) continue;
                 const int p_row = static_cast<unsigned>(pair[i]) < static_cast<unsigned>(a.pairs) ? pair[i] : -1;
                 __syncwarp();
-                if (a.gated) {
+                if (!kPairs && a.gated) {
                     // gate lanes take the first 8 rows, up lanes the others
                     const bool up = lane & 8;
                     uint16_t* col = reinterpret_cast<uint16_t*>(out) + ((lane >> 4) * 8 + (lane & 7)) + (up ? 8 * (kYRowGated / 2) : 0);
@@ -547,7 +548,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
                     const int n = ct * (kColsL / 2) + quarter * 16 + (lane & 1) * 8;
                     const uint4 v4 = *reinterpret_cast<const uint4*>(out + (lane >> 1) * kYRowGated + (lane & 1) * 16);
                     if (p >= 0 && n < n_out) *reinterpret_cast<uint4*>(a.y + static_cast<size_t>(p) * n_out + n) = v4;
-                } else if (a.y32) {
+                } else if (kPairs) {
                     // 8 rows x 32 columns at a time, a row of 128 bytes
                     float* col = reinterpret_cast<float*>(out) + lane;
 #pragma unroll
@@ -605,21 +606,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
 
 }  // namespace
 
+namespace {
+
+template <int SL>
+cudaError_t configure_sl() {
+    const cudaError_t e = cudaFuncSetAttribute(experts_large_kernel<SL, false>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemL);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(experts_large_kernel<SL, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemL);
+}
+
+template <int SL>
+cudaError_t launch_sl(const LargeArgs& l, int grid, cudaStream_t st) {
+    if (l.e.y32) experts_large_kernel<SL, true><<<grid, kLThreads, kSmemL, st>>>(l);
+    else experts_large_kernel<SL, false><<<grid, kLThreads, kSmemL, st>>>(l);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
 cudaError_t configure_experts_large() {
-    cudaError_t e = cudaFuncSetAttribute(experts_large_kernel<0>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemL);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(experts_large_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemL);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(experts_large_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemL);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(experts_large_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemL);
+    cudaError_t e = configure_sl<0>();
+    if (e == cudaSuccess) e = configure_sl<1>();
+    if (e == cudaSuccess) e = configure_sl<2>();
+    if (e == cudaSuccess) e = configure_sl<4>();
     return e;
 }
 
 cudaError_t launch_experts_large(const ExpertArgs& a, const DeviceInfo& d, cudaStream_t st) {
     const LargeArgs l{a, d.timeout_ns};
-    if (a.g == a.K) experts_large_kernel<0><<<d.num_sms & ~1, kLThreads, kSmemL, st>>>(l);
-    else if (a.g == 64) experts_large_kernel<2><<<d.num_sms & ~1, kLThreads, kSmemL, st>>>(l);
-    else if (a.g == 32) experts_large_kernel<4><<<d.num_sms & ~1, kLThreads, kSmemL, st>>>(l);
-    else experts_large_kernel<1><<<d.num_sms & ~1, kLThreads, kSmemL, st>>>(l);
-    return cudaGetLastError();
+    const int grid = d.num_sms & ~1;
+    if (a.g == a.K) return launch_sl<0>(l, grid, st);
+    if (a.g == 64) return launch_sl<2>(l, grid, st);
+    if (a.g == 32) return launch_sl<4>(l, grid, st);
+    return launch_sl<1>(l, grid, st);
 }
 
 }  // namespace wq
