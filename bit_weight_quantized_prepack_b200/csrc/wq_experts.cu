@@ -558,6 +558,12 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
     *reinterpret_cast<uint2*>(Y + t * N + n) = out;
 }
 
+static_assert(Small<0, 24>::kFixed + Small<0, 24>::rows_bytes(9984) <= Small<0, 24>::kMost &&
+                  Small<0, 24>::kFixed + Small<0, 24>::rows_bytes(9984 + kTileK) > Small<0, 24>::kMost &&
+                  Small<0, 16>::kFixed + Small<0, 16>::rows_bytes(11136) <= Small<0, 16>::kMost &&
+                  Small<0, 16>::kFixed + Small<0, 16>::rows_bytes(11136 + kTileK) > Small<0, 16>::kMost,
+              "the longest rows that launch_experts names");
+
 template <class C>
 cudaError_t configure_small() {
     const cudaError_t e = cudaFuncSetAttribute(experts_kernel<C, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -637,18 +643,20 @@ cudaError_t configure_expert_kernels() {
     return e;
 }
 
-// Rows per expert, were the pairs spread evenly, up to which mma.sync tiles of 8 rows beat the tcgen05
-// tiles, whose time is that of the dequantised weight and of each group's sums up to some hundred rows.
-// Measured (tiles of 8 rows against tcgen05 tiles): g = 128, 64 experts of 2048 x 2048: 12 rows 60.0 us
-// against 65.1, 16 rows 74.9 / 65.4; 8 of 4096 x 8192: 61.6 / 71.4, 70.8 / 70.9; g = K, 32 of 2048 x
-// 2048: 12 rows 34.7 / 36.2, 16 rows 39.7 / 36.3. g = 64, 128 of 1024 x 1536: 20 rows 74.1 / 81.2, 24
-// rows 83.8 / 82.1. g = 32, 32 of 2048 x 2048: 32 rows 70.3 / 97.8, 96 rows 180 / 137.
-int few_rows(const ExpertArgs& a) { return a.g == 32 ? 48 : a.g == 64 ? 22 : 14; }
+// Rows per expert, were the pairs spread evenly over all E, up to which mma.sync tiles of 8 rows beat the
+// tcgen05 tiles, whose time is that of the dequantised weight and of each group's sums up to some hundred
+// rows. Pairs of other devices' experts and padded places count here, since only the device knows them.
+// Measured from a cold L2 (tiles of 8 rows against tcgen05 tiles): g = 128, 64 experts of 2048 x 2048: 16 rows
+// 67.5 us against 67.5; 8 of 4096 x 8192: 16 rows 66.8 / 72.3, 20 rows 88.2 / 73.2; g = K, 32 of 2048 x
+// 2048: 12 rows 38.1 / 38.0, 16 rows 39.6 / 38.5, 20 rows 50.3 / 38.8. g = 64, 128 of 1024 x 1536: 24 rows 82.8
+// / 93.2, 28 rows 104 / 94. g = 32, 32 of 2048 x 2048: 48 rows 103 / 121, 64 rows 129 / 128; 128 of 1024 x
+// 1536: 48 rows 160 / 167, 56 rows 182 / 179.
+int few_rows(const ExpertArgs& a) { return a.g == 32 ? 48 : a.g == 64 ? 24 : 16; }
 
 cudaError_t launch_experts(const ExpertArgs& a, const DeviceInfo& d, cudaStream_t st) {
     const long long per_expert = (static_cast<long long>(a.pairs) + a.E - 1) / a.E;
     if (experts_token_form(a.pairs, a.E)) return launch_token<false>(a, nullptr, nullptr, 1, d.num_sms, st);
-    // rows of 16 warps' places reach further than those of 24: K up to 11008 against 9728
+    // rows of 16 warps' places reach further than those of 24: K up to 11136 against 9984
     if (per_expert > few_rows(a) || Small<0, 16>::places(a.K) == 0) return launch_experts_large(a, d, st);
     if (Small<0, 24>::places(a.K)) return launch_w<24>(a, d.num_sms, st);
     return launch_w<16>(a, d.num_sms, st);
