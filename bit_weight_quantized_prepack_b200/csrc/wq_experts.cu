@@ -11,7 +11,7 @@
 // fp32 partial, so no weight is rounded. A tile whose k-blocks lie with several warps is summed by the
 // one that has the first, in the order of the warps. The rows stay in shared memory because every SM
 // wants the same few at the same time: through a ring per warp 16 tokens over 2 of 8 experts of 4096 x
-// 22016 took 148 us, with the ring filled through L1 85. Now 72.6 us, 357 MB at 4.9 TB/s; 24 tokens
+// 22016 took 148 us, with the ring filled through L1 85. Now 72.4 us, 357 MB at 4.9 TB/s; 24 tokens
 // over 6 of 60 of 4096 x 1400, g = 64: 42 us, 167 MB at 4.0 TB/s. Without rows and MMAs the streams
 // reach 0.80 to 0.89 of the copy rate; the rest is the dequantisation's instructions, which grow with
 // the scales of a k-block.
@@ -519,7 +519,8 @@ __global__ void __launch_bounds__(512, 1) experts_token_kernel(ExpertArgs a, con
 // [0, E) adds nothing and its row is not read. The pairs' products come unrounded: a rounding of each
 // to fp16 would add to the output's own (1.4 times as far from the exact sum), and a product beyond
 // 65504 would be lost although its weighted sum is finite. One thread per 4 columns of a token, four
-// choices' rows under way at a time. Bound by the pairs' bytes.
+// choices' rows under way at a time. Bound by the pairs' bytes: 4096 tokens, 8 choices of 2048 columns,
+// 268 MB read and 17 MB written in 46 us, 6.2 TB/s.
 __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ yp, const int32_t* __restrict__ idx,
                                                       const float* __restrict__ w, int top_k, int E, int N,
                                                       uint16_t* __restrict__ Y, long long total) {

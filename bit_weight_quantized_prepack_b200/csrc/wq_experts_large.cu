@@ -20,11 +20,11 @@
 // (probe, 128 x 256 x 16: 137 cycles against 168). TMA gather4 in place of cp.async moves a row of 128
 // bytes per 14 cycles and set the pace at a quarter of this kernel's rate. The pair halves the rows'
 // way from L2, which one CTA alone loaded to two thirds.
-// Measured: 4096 tokens over 8 of 128 experts, g = 128: gated 2048 x 1536 275 us (750 TFLOP/s, 0.46 of
-// the dense rate), 768 x 2048 with the sum of pairs 197 us; 300 tokens over 2 of 8 of 11008 x 4096 116
-// us. Bound by instruction issue (two thirds of all slots, the adding and dequantising warps'): the
-// groups' sums are ready when the adding warps come to them, and the tensor pipe is busy 0.27 of the
-// time (768 x 2048).
+// Measured: 4096 tokens over 8 of 128 experts, g = 128: gated 2048 x 1536 283 us (730 TFLOP/s, 0.44 of
+// the dense rate), 768 x 2048 with the sum of pairs 222 us; 300 tokens over 2 of 8 of 11008 x 4096 120
+// us. No unit is full (2048 x 1536 / 768 x 2048): 74 / 65 % of the issue slots, 52 / 45 % of the integer pipe, 37 /
+// 28 % of the tensor pipe, 20 / 22 % of L2. The groups' sums are ready when the adding warps come to them:
+// the pace is that of the chains of load, wait and arithmetic in the adding and dequantising warps.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
