@@ -19,7 +19,7 @@ namespace {
 
 using namespace wq;
 
-constexpr int kVersion = 10000;  // 1.0.0
+constexpr int kVersion = 10100;  // 1.1.0
 constexpr unsigned long long kDefaultTimeoutNs = 2000000000ull;
 // W4A8 accumulates a * 16(q - 8) in int32; |a * 16(q - 8)| <= 128 * 128 = 16384 (a = -128,
 // q = 0), and K * 16384 < 2^31 holds for every multiple of 128 up to 130944.

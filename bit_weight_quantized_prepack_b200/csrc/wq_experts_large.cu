@@ -604,10 +604,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLThreads, 1) expert
     }
 }
 
-}  // namespace
-
-namespace {
-
 template <int SL>
 cudaError_t configure_sl() {
     const cudaError_t e = cudaFuncSetAttribute(experts_large_kernel<SL, false>,

@@ -69,7 +69,8 @@ typedef enum {
 /* Human-readable name of a status code. Never NULL. */
 WQ_API const char* wq_status_string(int status);
 
-/* Library version: major*10000 + minor*100 + patch. */
+/* Library version: major*10000 + minor*100 + patch. 1.1.0: wq_route_experts takes its scale as a double, and
+ * wq_gemm_w4a16_experts_combine's scratch holds fp32 products (callers of before must be compiled anew). */
 WQ_API int wq_version(void);
 
 /* ---------------------------------------------------------------- prepack (the layout pass)

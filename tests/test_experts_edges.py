@@ -92,3 +92,7 @@ def test_header_and_library_have_the_expert_entry_points():
                  "wq_unpack_experts", "wq_gemm_w4a16_experts", "wq_experts_scratch_bytes",
                  "wq_gemm_w4a16_experts_combine"):
         assert name in declared and hasattr(raw, name) and name in wq.__all__
+
+
+def test_the_version_tells_of_the_changed_signature():
+    assert wq.wq_version() >= 10100
