@@ -12,6 +12,7 @@ using namespace wq;
 
 constexpr long long kMaxTokens = 1ll << 24;
 constexpr long long kMaxPairs = 1ll << 28;
+constexpr int kMaxN = 0x7FFFFFFF - 255;  // columns rounded up to those of a tile must be an int
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -32,7 +33,7 @@ int check_counts(int T, int E, int top_k) {
 
 int check_weight(int E, int K, int N, int g, int gated) {
     if (E <= 0 || K <= 0 || N <= 0 || (gated != 0 && gated != 1)) return WQ_ERR_INVALID_ARG;
-    if (E > kExMaxExperts || !shape_ok(K, N) || (gated && N % 16)) return WQ_ERR_UNSUPPORTED_SHAPE;
+    if (E > kExMaxExperts || !shape_ok(K, N) || (gated && N % 16) || N > kMaxN) return WQ_ERR_UNSUPPORTED_SHAPE;
     if (scale_slots(K, g) < 0) return WQ_ERR_INVALID_ARG;
     return WQ_OK;
 }

@@ -283,8 +283,8 @@ WQ_API int wq_gemm_w4a16_noalloc(const uint16_t* A, const void* Wp, uint16_t* Y,
  * ("Atom: Low-bit Quantization for Efficient and Accurate LLM Serving", method: fine-grained
  * group quantisation, here of every expert's weight; the routing is not in the pages.)
  * Limits: 1 <= E <= 1024, 1 <= top_k <= 32 (for the routing also top_k <= E), 0 <= T <= 2^24,
- * T * top_k <= 2^28; T == 0 computes nothing. Alignment: A, H, Wp, Y, Q, s, scratch 16 bytes; idx, w, bias, offsets, rows
- * and fp32 logits 4 bytes, fp16 logits 2 bytes. No call here uses the library's workspace, so
+ * T * top_k <= 2^28, N <= 2^31 - 256; T == 0 computes nothing. Alignment: A, H, Wp, Y, Q, s, scratch
+ * 16 bytes; idx, w, bias, offsets, rows and fp32 logits 4 bytes, fp16 logits 2 bytes. No call here uses the library's workspace, so
  * calls and captured graphs that run at the same time share nothing but what the caller gives
  * them both. Results are deterministic.
  *

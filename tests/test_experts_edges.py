@@ -96,3 +96,12 @@ def test_header_and_library_have_the_expert_entry_points():
 
 def test_the_version_tells_of_the_changed_signature():
     assert wq.wq_version() >= 10100
+
+
+@pytest.mark.parametrize("N", [2 ** 31 - 8, 2 ** 31 - 40, 2 ** 31 - 248])
+def test_columns_whose_tiles_pass_an_int_are_refused(N):
+    assert wq.wq_prepacked_bytes_experts(1, 128, N, 128) == 0
+    ok = ctypes.c_void_p(0x10000)  # never dereferenced
+    assert wq.lib.wq_gemm_w4a16_experts(ok, ok, ok, ctypes.c_void_p(0x10002), ok, 4, 1, 1, N, 128, 128, 0,
+                                        None) == wq.WQ_ERR_UNSUPPORTED_SHAPE
+    assert wq.wq_prepacked_bytes_experts(1, 128, 2 ** 31 - 256, 128) >= 64 * (2 ** 31 - 256)
